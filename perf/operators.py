@@ -297,8 +297,10 @@ def _own(st, op):
     from paged_kv_cache_336_b200 import binding
     case = st["case"]
     if op == "extend":
+        if "next" not in st:  # a serving loop keeps two sets of a step's outputs and swaps them
+            st["next"] = binding.StepTables.empty(case["B"], st["max_tokens"])
         r = binding.extend_tables(st["tables"], st["ctx"], st["new"], st["queue"], st["queue_state"],
-                                  case["bs"], st["max_tokens"])
+                                  case["bs"], st["max_tokens"], out=st["next"])
         return [st["tables"], r.context_lens, r.query_start, r.positions, r.slot_mapping, r.queue_state, st["queue"]]
     if op == "rope":
         q = binding.rope_append(st["q"], st["k"], st["v"], st["positions"], st["inv_freq"], st["slots"],
