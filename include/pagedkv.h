@@ -73,6 +73,9 @@ typedef enum { PA_F32 = 0, PA_BF16 = 1 } pa_dtype_t;
 #define PA_DEVERR_SLOT 0x4u         /* slot >= num_blocks * block_size */
 #define PA_DEVERR_COPY_PAIR 0x8u    /* copy pair index outside [0, num_blocks) */
 #define PA_DEVERR_TIMEOUT 0x10u     /* a pipeline wait hit its time limit; output invalid */
+#define PA_DEVERR_NO_FREE_BLOCKS 0x20u /* pa_extend_tables: the free queue cannot supply the batch */
+#define PA_DEVERR_NUM_TOKENS 0x40u  /* pa_extend_tables: more new tokens than max_tokens */
+#define PA_DEVERR_FREE_QUEUE 0x80u  /* pa_extend_tables: queue state outside its ring, or no room for returned blocks */
 
 /* Library version string, e.g. "pagedkv 0.1 sm_100a". */
 const char* pa_version(void);
@@ -269,6 +272,25 @@ pa_status_t pa_decode_split_window(const void* q, const void* k_pool, const void
                                    void* stream);
 
 /* ---------------------------------------------------------------------------
+ * pa_decode_split_sinks - sliding-window decode with sinks: as
+ * pa_decode_split_window, but the first `num_sinks` tokens of each sequence
+ * stay visible beside the window, so the query attends to tokens t < ctx with
+ * t >= ctx - window or t < num_sinks (window >= 1, num_sinks >= 0). Blocks
+ * that hold neither a sink nor a token of the window are never read and their
+ * table entries may be -1. fp32 and bf16, the shapes of pa_decode_split; runs
+ * on the balanced kernel whatever the table size (the partitions of the other
+ * cut are runs of consecutive blocks). Same workspace and contract as
+ * pa_decode_split.
+ * ------------------------------------------------------------------------- */
+pa_status_t pa_decode_split_sinks(const void* q, const void* k_pool, const void* v_pool,
+                                  const int32_t* block_tables, const int32_t* context_lens,
+                                  int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                  int block_size, int num_blocks, int max_blocks_per_seq,
+                                  float scale, pa_dtype_t dtype, int partition_tokens, int window,
+                                  int num_sinks, void* workspace, size_t workspace_bytes,
+                                  void* out, uint32_t* dev_err, void* stream);
+
+/* ---------------------------------------------------------------------------
  * pa_prefill - causal (chunked) prefill attention over the paged cache.
  * Sequence s holds context_lens[s] tokens, the last query_lens[s] of them
  * new (their K and V already written, e.g. by pa_kv_append); its queries are
@@ -380,6 +402,204 @@ pa_status_t pa_kv_append(const void* k_new, const void* v_new,
 pa_status_t pa_copy_blocks(void* k_pool, void* v_pool, const int64_t* src_dst_pairs,
                            int num_pairs, size_t block_bytes, int num_blocks,
                            uint32_t* dev_err, void* stream);
+
+/* ===========================================================================
+ * 4-bit KV cache. Each pool is uint8 [num_blocks][num_kv_heads][tile], with
+ * tile = pa_q4_tile_bytes(block_size, head_dim) = block_size / 16 * 9 *
+ * head_dim bytes (4.5 bits a value). pa_copy_blocks, pa_swap_out and
+ * pa_swap_in move such blocks as they are (block_bytes = num_kv_heads * tile).
+ * head_dim 64, 128 or 256, block_size 16 or 32.
+ *
+ * The 64 dims 64 i .. 64 i + 63 of one (token, KV head) are a group:
+ *     mn = min x,  s = bf16((max x - mn) / 15),
+ *     code = rint((x - mn) / s) in 0..15 (ties to even; 0 when s = 0),
+ *     value = mn + s * code.
+ * x is bf16, so mn is exact in bf16. A group that holds a NaN or an infinity
+ * gets s = mn = NaN: all of its values read NaN.
+ *
+ * A tile is block_size / 16 sub-tiles of 16 tokens (token t of the block in
+ * sub-tile t / 16, row r = t % 16). A sub-tile is
+ *     codes   [16][head_dim / 2] bytes,
+ *     params  [16][head_dim / 64] pairs (s, mn) of bf16.
+ * Dims 8 c .. 8 c + 7 are one little-endian 32-bit word of a code row, dim 8 c
+ * in its lowest 4 bits. With group i = c / 8, the word's byte offset is
+ *   K: t = (c / 2) % 4, w = 2 i + c % 2:
+ *      head_dim 64: 8 t + 4 w;  128: 16 t + 4 w;
+ *      256: 64 ((w / 4) ^ (r % 2)) + 16 t + 4 (w % 4);
+ *   V: g = c % 8:
+ *      head_dim 64: 4 g;  128: 8 (g ^ 4 ((r / 2) % 2)) + 4 i;
+ *      256: 16 (g ^ 2 (r % 4)) + 4 i.
+ * ========================================================================= */
+
+/* Bytes of one (block, KV head) tile of one pool; 0 for unsupported sizes. */
+size_t pa_q4_tile_bytes(int block_size, int head_dim);
+
+/* ---------------------------------------------------------------------------
+ * pa_kv_append_q4 - pa_kv_append into a 4-bit cache. k_new, v_new:
+ * [num_tokens][num_kv_heads][head_dim] bf16 (dtype PA_BF16), heads and dims
+ * contiguous, tokens k_stride / v_stride elements apart (multiples of 16
+ * bytes). Slots as for pa_kv_append: negative ones write nothing, duplicates
+ * race. Only the slots' own rows change.
+ * ------------------------------------------------------------------------- */
+pa_status_t pa_kv_append_q4(const void* k_new, const void* v_new, int64_t k_stride,
+                            int64_t v_stride, const int64_t* slot_mapping, int num_tokens,
+                            int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                            pa_dtype_t dtype, void* k_pool, void* v_pool, uint32_t* dev_err,
+                            void* stream);
+
+/* ---------------------------------------------------------------------------
+ * pa_kv_gather_q4 - reads rows of a 4-bit cache back: k_out, v_out
+ * [num_tokens][num_kv_heads][head_dim] in dtype (PA_F32 or PA_BF16), row t the
+ * values of slot_mapping[t] (rounded once for bf16). A row with a negative
+ * slot is left as it was. A slot may appear any number of times. With slots
+ * in token order it lays a sequence out for pa_prefill's 16-bit pools
+ * (pa_kv_append) or for inspection.
+ * ------------------------------------------------------------------------- */
+pa_status_t pa_kv_gather_q4(const void* k_pool, const void* v_pool, const int64_t* slot_mapping,
+                            int num_tokens, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, pa_dtype_t dtype, void* k_out, void* v_out,
+                            uint32_t* dev_err, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * pa_decode_q4 - single-query decode attention over a 4-bit cache: the result
+ * of pa_decode_split (window = 0), pa_decode_split_window (window >= 1,
+ * num_sinks = 0) or pa_decode_split_sinks on the values that the pools stand
+ * for. q and out bf16 (dtype PA_BF16), any group size 1..16, head_dim 64, 128
+ * or 256. num_sinks without a window changes nothing.
+ *
+ * Arithmetic: logits in fp32 from products of bf16 queries with the codes
+ * (exact integers); softmax weights times the values' scales are rounded to
+ * bf16 before the product with the value codes, as P is in the bf16 path;
+ * minima enter in fp32. Key and value scales up to 2^100.
+ *
+ * workspace, partition_tokens: the contract of pa_decode_split with the same
+ * sizes; the work is cut as for its long tables (equal runs of 16-token
+ * units), whatever the table size. num_seqs <= 4096.
+ * ------------------------------------------------------------------------- */
+pa_status_t pa_decode_q4(const void* q, const void* k_pool, const void* v_pool,
+                         const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                         int num_blocks, int max_blocks_per_seq, float scale, pa_dtype_t dtype,
+                         int window, int num_sinks, int partition_tokens, void* workspace,
+                         size_t workspace_bytes, void* out, uint32_t* dev_err, void* stream);
+
+/* ===========================================================================
+ * Rotary positions with the cache write.
+ * ========================================================================= */
+typedef enum {
+  PA_ROPE_NONE = 0,
+  PA_ROPE_LINEAR = 1, /* positions divided by factor */
+  PA_ROPE_NTK = 2,    /* base stretched by factor^(rotary_dim / (rotary_dim - 2)) */
+  PA_ROPE_YARN = 3    /* per-pair ramp between kept and divided frequencies */
+} pa_rope_scaling_t;
+
+/* Inverse frequencies for pa_rope_append: inv_freq[i] = base^(-2 i /
+ * rotary_dim), i < rotary_dim / 2 (host memory, computed in double), scaled
+ * for long contexts:
+ *   LINEAR  inv_freq / factor;
+ *   NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in base's place;
+ *   YARN    with dim(n) = rotary_dim * log(original_context / (2 pi n)) /
+ *           (2 log base), low = max(floor(dim(beta_fast)), 0), high =
+ *           min(ceil(dim(beta_slow)), rotary_dim - 1) and r = clamp((i - low) /
+ *           max(high - low, 0.001), 0, 1): inv_freq / factor * r + inv_freq *
+ *           (1 - r), and *mscale = 0.1 log(factor) + 1.
+ * *mscale is 1 for the others. factor >= 1; original_context, beta_fast >
+ * beta_slow > 0 are read for YARN only. Host only. */
+pa_status_t pa_rope_frequencies(int rotary_dim, double base, pa_rope_scaling_t scaling,
+                                double factor, int original_context, double beta_fast,
+                                double beta_slow, float* inv_freq, float* mscale);
+
+/* ---------------------------------------------------------------------------
+ * pa_rope_append - rotates the new tokens' queries and keys by their
+ * positions and writes keys and values into their slots, in one pass. For
+ * token t at position p = positions[t] (int32) and pair i < rotary_dim / 2 of
+ * every query and key head, with c = mscale cos(p * inv_freq[i]), s = mscale
+ * sin(p * inv_freq[i]):
+ *     a' = c a - s b,   b' = c b + s a
+ * where (a, b) are dims (i, i + rotary_dim / 2), or with `interleaved` non-zero
+ * dims (2 i, 2 i + 1); dims from rotary_dim on are unchanged. Angles are
+ * reduced in double, so far positions keep fp32 accuracy; the rotation is
+ * fp32, rounded once. inv_freq: device fp32 [rotary_dim / 2].
+ *
+ * q [num_tokens][num_q_heads][head_dim], k_new and v_new
+ * [num_tokens][num_kv_heads][head_dim] in dtype, heads and dims contiguous,
+ * tokens q_stride, k_stride, v_stride elements apart (multiples of 16 bytes:
+ * views of one fused product will do). q_out: contiguous
+ * [num_tokens][num_q_heads][head_dim]; it may be q itself if that is
+ * contiguous, and overlaps no other input. Pools, slots: as for pa_kv_append
+ * (pools in dtype). A token with a negative slot is padding: its q is rotated,
+ * nothing is cached. num_q_heads may be 0 (q and q_out are then not read).
+ * rotary_dim: a multiple of 16, 0 .. head_dim; head_dim 64, 128 or 256,
+ * block_size 16 or 32.
+ *
+ * pa_rope_append_q4 - the same into 4-bit pools (PA_BF16 only): keys are
+ * rotated, rounded to bf16 and then quantised as by pa_kv_append_q4.
+ * ------------------------------------------------------------------------- */
+pa_status_t pa_rope_append(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                           const float* inv_freq, const int64_t* slot_mapping, int num_tokens,
+                           int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                           int interleaved, float mscale, int block_size, int num_blocks,
+                           pa_dtype_t dtype, void* q_out, void* k_pool, void* v_pool,
+                           uint32_t* dev_err, void* stream);
+pa_status_t pa_rope_append_q4(const void* q, const void* k_new, const void* v_new,
+                              int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              const int32_t* positions, const float* inv_freq,
+                              const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                              int num_kv_heads, int head_dim, int rotary_dim, int interleaved,
+                              float mscale, int block_size, int num_blocks, pa_dtype_t dtype,
+                              void* q_out, void* k_pool, void* v_pool, uint32_t* dev_err,
+                              void* stream);
+
+/* ---------------------------------------------------------------------------
+ * pa_extend_tables - a step's bookkeeping on the GPU: from the lengths of its
+ * requests it takes blocks from a device free queue, extends the block tables
+ * and writes positions and slots for every new token, in one launch (no host
+ * round trip, so a step can be captured into a CUDA graph).
+ *
+ * new_lens[s] >= 0: sequence s receives that many tokens, for which it takes
+ * ceil((ctx + new) / block_size) - ceil(ctx / block_size) blocks; -1: the
+ * sequence leaves, its blocks go back to the queue and its length becomes 0
+ * (its table row is left as it was; entries of -1, blocks released before a
+ * window, are passed over). Blocks are taken from the queue's front
+ * and returned to its back in sequence order, as the host block manager does
+ * (within a sequence in table order, where that manager goes by block id).
+ * Reference counts stay with that manager: a sequence extended or released
+ * here shares no block with another.
+ *
+ *   block_tables      int32 [num_seqs][max_blocks_per_seq], in/out: only new
+ *                     entries are written
+ *   context_lens, new_lens  int32 [num_seqs], in
+ *   free_queue        int32 [num_blocks], in/out: a ring; queue_state (in,
+ *                     int32 [2]) holds (head, count), the free blocks being
+ *                     entries head .. head + count - 1 mod num_blocks
+ *   context_lens_out  int32 [num_seqs]: lengths after the step
+ *   query_start       int32 [num_seqs + 1]: first token row of each sequence,
+ *                     then the number of tokens
+ *   positions         int32 [max_tokens], slot_mapping int64 [max_tokens]: of
+ *                     each new token, sequence after sequence; rows past the
+ *                     last token are padding (position 0, slot -1). Both
+ *                     16-byte aligned
+ *   queue_state_out   int32 [2]
+ * Outputs may not share memory with one another or with the inputs marked in
+ * (a loop keeps two sets and swaps them).
+ *
+ * All or nothing: if a length is out of range (negative, new_lens below -1,
+ * past the table), the queue cannot supply the blocks (blocks returned by the
+ * same call do not count), its state lies outside the ring or has no room
+ * for the returned blocks, or there are more than max_tokens tokens, the
+ * PA_DEVERR_* bits are set, tables and queue stay as they are, lengths and
+ * queue state are passed through, query_start is zero and every token row is
+ * padding. A block id outside [0, num_blocks) in a table or the queue sets
+ * PA_DEVERR_BLOCK_ID, gives its tokens slot -1 and is never returned to the
+ * queue. num_seqs <= 4096.
+ * ------------------------------------------------------------------------- */
+pa_status_t pa_extend_tables(int32_t* block_tables, const int32_t* context_lens,
+                             const int32_t* new_lens, int num_seqs, int max_blocks_per_seq,
+                             int block_size, int32_t* free_queue, int num_blocks,
+                             const int32_t* queue_state, int max_tokens, int32_t* context_lens_out,
+                             int32_t* query_start, int32_t* positions, int64_t* slot_mapping,
+                             int32_t* queue_state_out, uint32_t* dev_err, void* stream);
 
 /* ===========================================================================
  * Host block manager ([Q] How It Works; [G] sections 2 and 4).

@@ -22,6 +22,9 @@ Modules
     Reference host block manager: FIFO free queue, reference counts,
     per-sequence block tables, copy-on-write on append, all-or-nothing
     failure.
+``serving_ops``
+    The operators around a step: window with sinks, the 4-bit cache's
+    quantisation and layout, rotary positions, block tables from lengths.
 
 Sources (web pages on PagedAttention; cited by page title and section):
 
@@ -46,6 +49,15 @@ from .paged_attention import (  # noqa: F401
     partitioned_decode_one,
     kv_append,
     copy_blocks,
+)
+from .serving_ops import (  # noqa: F401
+    extend_tables,
+    paged_decode_sinks,
+    q4_dense,
+    q4_quantize,
+    q4_read,
+    q4_write,
+    rope,
 )
 from .block_manager import (  # noqa: F401
     BlockManager,

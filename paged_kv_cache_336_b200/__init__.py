@@ -19,10 +19,19 @@ from .binding import (  # noqa: F401
     decode,
     decode_split,
     decode_split_window,
+    decode_split_sinks,
+    decode_q4,
     decode_shared_prefix,
     prefill,
     decode_split_workspace_size,
     kv_append,
+    kv_append_q4,
+    kv_gather_q4,
+    q4_pools,
+    rope_append,
+    rope_frequencies,
+    extend_tables,
+    StepTables,
     copy_blocks,
     swap_out,
     swap_in,

@@ -31,6 +31,11 @@ DEVERR_CONTEXT_LEN = 0x2
 DEVERR_SLOT = 0x4
 DEVERR_COPY_PAIR = 0x8
 DEVERR_TIMEOUT = 0x10
+DEVERR_NO_FREE_BLOCKS = 0x20
+DEVERR_NUM_TOKENS = 0x40
+DEVERR_FREE_QUEUE = 0x80
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class PagedKVError(RuntimeError):
@@ -63,6 +68,7 @@ _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
+_D = ctypes.c_double
 
 
 class StepBuffers(ctypes.Structure):
@@ -108,6 +114,19 @@ _SIGNATURES = {
     "pa_swap_in": (_I, [_P, _P, _P, _P, _P, _I, _SZ, _I, _I, _P, _P]),
     "pa_decode_split_window": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I,
                                     _I, _P, _SZ, _P, _P, _P]),
+    "pa_decode_split_sinks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I,
+                                   _I, _I, _P, _SZ, _P, _P, _P]),
+    "pa_q4_tile_bytes": (_SZ, [_I, _I]),
+    "pa_kv_append_q4": (_I, [_P, _P, _I64, _I64, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "pa_kv_gather_q4": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "pa_decode_q4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _I, _P,
+                          _SZ, _P, _P, _P]),
+    "pa_rope_frequencies": (_I, [_I, _D, _I, _D, _I, _D, _D, _P, ctypes.POINTER(_F)]),
+    "pa_rope_append": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F,
+                            _I, _I, _I, _P, _P, _P, _P, _P]),
+    "pa_rope_append_q4": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                               _F, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "pa_extend_tables": (_I, [_P, _P, _P, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P]),
     "pa_kv_append": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
     "pa_copy_blocks": (_I, [_P, _P, _P, _I, _SZ, _I, _P, _P]),
     "pa_bm_create": (_I, [_I, _I, _I, _P, ctypes.POINTER(_P)]),
@@ -437,6 +456,272 @@ def copy_blocks(k_pool, v_pool, src_dst_pairs, dev_err=None, stream=None):
     _check(library().pa_copy_blocks(
         _ptr(k_pool), _ptr(v_pool), _ptr(src_dst_pairs), src_dst_pairs.shape[0], block_bytes, NB,
         _ptr(dev_err), _stream_ptr(stream)))
+
+
+# ---------------------------------------------------------------------------
+# 4-bit cache, sinks, rotary positions, step bookkeeping. These calls sit in
+# decode loops of small batches, where the host's time counts: each argument
+# is looked at once.
+
+def _bad(msg):
+    return InvalidArgumentError(PA_ERR_INVALID_ARG, msg)
+
+
+def _on_device(device, *tensors):
+    """Contiguous tensors on `device`, which is the current one."""
+    torch = _torch()
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise _bad("tensors must be on the current CUDA device")
+    for t in tensors:
+        if t is not None and (t.device != device or not t.is_contiguous()):
+            raise _bad("tensors must be contiguous and on one CUDA device")
+
+
+def _token_rows(t, heads, head_dim, what):
+    """Elements between the tokens of a [tokens, heads, head_dim] tensor whose
+    heads and dims are contiguous (a slice of a fused product, or whole)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise _bad(f"{what} must be [tokens, {heads}, {head_dim}]")
+    st, sh, sd = t.stride()
+    if (sd != 1 and head_dim != 1) or (sh != head_dim and heads > 1):
+        raise _bad(f"{what}: heads and dims must be contiguous")
+    return st if t.shape[0] > 1 else heads * head_dim
+
+
+def decode_split_sinks(q, k_pool, v_pool, block_tables, context_lens, scale: float, window: int,
+                       sinks: int, partition_tokens: int = 512, out=None,
+                       workspace: SplitWorkspace | None = None, dev_err=None, stream=None):
+    """pa_decode_split_sinks: attention over the last ``window`` tokens and the
+    first ``sinks``. A given workspace sets partition_tokens."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty_like(q)
+    B, Hq, D, NB, Hkv, BS, MBS = _decode_common(q, k_pool, v_pool, block_tables, context_lens, out)
+    if workspace is None:
+        workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
+    _check(library().pa_decode_split_sinks(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens), B, Hq, Hkv,
+        D, BS, NB, MBS, float(scale), _dtype_code(q), workspace.partition_tokens, int(window),
+        int(sinks), workspace.ptr, workspace.nbytes, _ptr(out), _ptr(dev_err),
+        _stream_ptr(stream)))
+    return out
+
+
+def q4_tile_bytes(block_size: int, head_dim: int) -> int:
+    """pa_q4_tile_bytes: bytes of one (block, KV head) tile of a 4-bit pool."""
+    n = library().pa_q4_tile_bytes(int(block_size), int(head_dim))
+    if n == 0:
+        raise PagedKVError(PA_ERR_UNSUPPORTED,
+                           f"no 4-bit cache for head_dim={head_dim} block_size={block_size}")
+    return int(n)
+
+
+def q4_pools(num_blocks, num_kv_heads, block_size, head_dim, device=None):
+    """A zeroed pair of 4-bit pools, uint8 [num_blocks, num_kv_heads, tile bytes]."""
+    torch = _torch()
+    shape = (int(num_blocks), int(num_kv_heads), q4_tile_bytes(block_size, head_dim))
+    device = device or torch.device("cuda")
+    return (torch.zeros(shape, dtype=torch.uint8, device=device),
+            torch.zeros(shape, dtype=torch.uint8, device=device))
+
+
+def _q4_pool_shape(k_pool, v_pool, head_dim):
+    """(num_blocks, num_kv_heads, block_size) of a pair of 4-bit pools."""
+    torch = _torch()
+    if (k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8 or k_pool.dim() != 3
+            or k_pool.shape != v_pool.shape):
+        raise _bad("4-bit pools must be two uint8 [num_blocks, num_kv_heads, tile bytes] tensors")
+    NB, Hkv, tile = k_pool.shape
+    BS = 16 * tile // (9 * head_dim)
+    if BS < 16 or tile != BS // 16 * 9 * head_dim:
+        raise _bad(f"tiles of {tile} bytes do not hold blocks of head_dim {head_dim}")
+    return NB, Hkv, BS
+
+
+def kv_append_q4(k_new, v_new, slot_mapping, k_pool, v_pool, dev_err=None, stream=None):
+    """pa_kv_append_q4: quantises new rows (bf16, heads and dims contiguous)
+    into their slots of 4-bit pools."""
+    torch = _torch()
+    T, Hkv, D = k_new.shape
+    NB, H2, BS = _q4_pool_shape(k_pool, v_pool, D)
+    _on_device(k_pool.device, k_pool, v_pool, slot_mapping)
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or H2 != Hkv:
+        raise _bad("slot_mapping must be int64 [tokens] and the pools' heads those of k_new")
+    if (v_new.shape != k_new.shape or k_new.dtype != v_new.dtype or k_new.device != k_pool.device
+            or v_new.device != k_pool.device):
+        raise _bad("k_new and v_new must match in shape, type and device")
+    _check(library().pa_kv_append_q4(
+        k_new.data_ptr(), v_new.data_ptr(), _token_rows(k_new, Hkv, D, "k_new"),
+        _token_rows(v_new, Hkv, D, "v_new"), slot_mapping.data_ptr(), T, Hkv, D, BS, NB,
+        _dtype_code(k_new), k_pool.data_ptr(), v_pool.data_ptr(), _ptr(dev_err),
+        _stream_ptr(stream)))
+
+
+def kv_gather_q4(k_pool, v_pool, slot_mapping, head_dim: int, dtype=None, out=None, dev_err=None,
+                 stream=None):
+    """pa_kv_gather_q4: the values of 4-bit rows, (k, v) of [tokens, heads,
+    head_dim] in ``dtype`` (bf16 unless given). Rows of negative slots keep what
+    ``out`` held (zeros if it is made here)."""
+    torch = _torch()
+    NB, Hkv, BS = _q4_pool_shape(k_pool, v_pool, head_dim)
+    _on_device(k_pool.device, k_pool, v_pool, slot_mapping)
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1:
+        raise _bad("slot_mapping must be int64 [tokens]")
+    T = slot_mapping.shape[0]
+    if out is None:
+        both = torch.zeros((2, T, Hkv, head_dim), dtype=dtype or torch.bfloat16, device=k_pool.device)
+        k_out, v_out = both[0], both[1]
+    else:
+        k_out, v_out = out
+        _on_device(k_pool.device, k_out, v_out)
+        if (k_out.shape != (T, Hkv, head_dim) or v_out.shape != k_out.shape
+                or v_out.dtype != k_out.dtype or (dtype is not None and dtype != k_out.dtype)):
+            raise _bad("out must be two [tokens, heads, head_dim] tensors of one type")
+    _check(library().pa_kv_gather_q4(
+        k_pool.data_ptr(), v_pool.data_ptr(), slot_mapping.data_ptr(), T, Hkv, int(head_dim), BS,
+        NB, _dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(), _ptr(dev_err),
+        _stream_ptr(stream)))
+    return k_out, v_out
+
+
+def decode_q4(q, k_pool, v_pool, block_tables, context_lens, scale: float, window: int = 0,
+              sinks: int = 0, partition_tokens: int = 512, out=None,
+              workspace: SplitWorkspace | None = None, dev_err=None, stream=None):
+    """pa_decode_q4: decode attention over 4-bit pools; ``window`` 0 sees the
+    whole context. A given workspace (SplitWorkspace) sets partition_tokens."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty_like(q)
+    B, Hq, D = q.shape
+    NB, Hkv, BS = _q4_pool_shape(k_pool, v_pool, D)
+    _on_device(q.device, q, k_pool, v_pool, block_tables, context_lens, out)
+    if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32
+            or block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,)):
+        raise _bad("block_tables must be int32 [seqs, blocks], context_lens int32 [seqs]")
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise _bad("out must match q")
+    MBS = block_tables.shape[1]
+    if workspace is None:
+        workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
+    _check(library().pa_decode_q4(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, MBS, float(scale), _dtype_code(q),
+        int(window), int(sinks), workspace.partition_tokens, workspace.ptr, workspace.nbytes,
+        out.data_ptr(), _ptr(dev_err), _stream_ptr(stream)))
+    return out
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, original_context: int = 4096, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device=None):
+    """pa_rope_frequencies: (inv_freq fp32 [rotary_dim / 2] on ``device``, mscale)."""
+    import numpy as np
+    torch = _torch()
+    if scaling not in ROPE_SCALINGS:
+        raise _bad(f"unknown scaling {scaling!r}")
+    inv = np.empty(max(int(rotary_dim), 0) // 2, dtype=np.float32)
+    m = _F()
+    _check(library().pa_rope_frequencies(int(rotary_dim), float(base), ROPE_SCALINGS[scaling],
+                                         float(factor), int(original_context), float(beta_fast),
+                                         float(beta_slow), inv.ctypes.data, ctypes.byref(m)))
+    return torch.from_numpy(inv).to(device or torch.device("cuda")), float(m.value)
+
+
+def rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_pool, v_pool,
+                interleaved: bool = False, mscale: float = 1.0, q_out=None, dev_err=None,
+                stream=None):
+    """pa_rope_append, or pa_rope_append_q4 when the pools are uint8: rotates q
+    and k by their positions and writes k and v into their slots. q may be
+    None; returns the rotated queries (None without q)."""
+    torch = _torch()
+    T, Hkv, D = k_new.shape
+    dev = k_pool.device
+    q4 = k_pool.dtype == torch.uint8
+    if q4:
+        NB, H2, BS = _q4_pool_shape(k_pool, v_pool, D)
+    else:
+        if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.shape[3] != D:
+            raise _bad("pools must be [num_blocks, num_kv_heads, block_size, head_dim]")
+        if k_pool.dtype != k_new.dtype or v_pool.dtype != k_new.dtype:
+            raise _bad("pools must have the type of k_new")
+        NB, H2, BS, _ = k_pool.shape
+    _on_device(dev, k_pool, v_pool, slot_mapping, positions, inv_freq)
+    if (positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64
+            or inv_freq.dtype != torch.float32 or positions.shape != (T,)
+            or slot_mapping.shape != (T,) or inv_freq.dim() != 1 or H2 != Hkv):
+        raise _bad("positions int32 [tokens], slot_mapping int64 [tokens], inv_freq fp32")
+    if (v_new.shape != k_new.shape or v_new.dtype != k_new.dtype or k_new.device != dev
+            or v_new.device != dev):
+        raise _bad("k_new and v_new must match in shape, type and device")
+    Hq = q_stride = 0
+    if q is not None:
+        Hq = q.shape[1]
+        if q.shape[0] != T or q.dtype != k_new.dtype or q.device != dev:
+            raise _bad("q must have the tokens, type and device of k_new")
+        q_stride = _token_rows(q, Hq, D, "q")
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        elif (q_out.shape != (T, Hq, D) or q_out.dtype != q.dtype or q_out.device != dev
+              or not q_out.is_contiguous()):
+            raise _bad("q_out must be contiguous, of q's shape and type")
+    fn = library().pa_rope_append_q4 if q4 else library().pa_rope_append
+    _check(fn(_ptr(q), k_new.data_ptr(), v_new.data_ptr(), q_stride,
+              _token_rows(k_new, Hkv, D, "k_new"), _token_rows(v_new, Hkv, D, "v_new"),
+              positions.data_ptr(), inv_freq.data_ptr(), slot_mapping.data_ptr(), T, Hq, Hkv, D,
+              2 * inv_freq.shape[0], 1 if interleaved else 0, mscale, BS, NB, _dtype_code(k_new),
+              _ptr(q_out), k_pool.data_ptr(), v_pool.data_ptr(), _ptr(dev_err),
+              _stream_ptr(stream)))
+    return q_out
+
+
+@dataclass
+class StepTables:
+    """What pa_extend_tables writes: lengths after the step, first token row of
+    each sequence (and the number of tokens), position and slot of every token,
+    and the free queue's state after the step."""
+    context_lens: object
+    query_start: object
+    positions: object
+    slot_mapping: object
+    queue_state: object
+
+    @classmethod
+    def empty(cls, num_seqs: int, max_tokens: int, device=None):
+        torch = _torch()
+        device = device or torch.device("cuda")
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.empty(num_seqs, **i32), torch.empty(num_seqs + 1, **i32),
+                   torch.empty(max_tokens, **i32),
+                   torch.empty(max_tokens, dtype=torch.int64, device=device), torch.empty(2, **i32))
+
+
+def extend_tables(block_tables, context_lens, new_lens, free_queue, queue_state, block_size: int,
+                  max_tokens: int, out: StepTables | None = None, dev_err=None, stream=None):
+    """pa_extend_tables: takes a step's blocks from the device free queue and
+    returns its StepTables. ``out`` shares nothing with the inputs: a loop keeps
+    two and swaps them."""
+    torch = _torch()
+    dev = block_tables.device
+    B, MBS = block_tables.shape
+    if out is None:
+        out = StepTables.empty(B, max_tokens, dev)
+    _on_device(dev, block_tables, context_lens, new_lens, free_queue, queue_state, out.context_lens,
+               out.query_start, out.positions, out.slot_mapping, out.queue_state)
+    i32 = torch.int32
+    for t, n in ((block_tables, B * MBS), (context_lens, B), (new_lens, B),
+                 (free_queue, free_queue.numel()), (queue_state, 2), (out.context_lens, B),
+                 (out.query_start, B + 1), (out.positions, max_tokens), (out.queue_state, 2)):
+        if t.dtype != i32 or t.numel() != n:
+            raise _bad("tables, lengths, queue and outputs must be int32 of the batch's sizes")
+    if out.slot_mapping.dtype != torch.int64 or out.slot_mapping.numel() != max_tokens:
+        raise _bad("slot_mapping must be int64 [max_tokens]")
+    _check(library().pa_extend_tables(
+        block_tables.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(), B, MBS,
+        int(block_size), free_queue.data_ptr(), free_queue.numel(), queue_state.data_ptr(),
+        int(max_tokens), out.context_lens.data_ptr(), out.query_start.data_ptr(),
+        out.positions.data_ptr(), out.slot_mapping.data_ptr(), out.queue_state.data_ptr(),
+        _ptr(dev_err), _stream_ptr(stream)))
+    return out
 
 
 # ---------------------------------------------------------------------------

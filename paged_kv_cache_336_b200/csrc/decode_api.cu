@@ -18,6 +18,7 @@
 
 #include "decode_dispatch.h"
 #include "decode_kernel.cuh"
+#include "decode_sinks_kernel.cuh"
 #include "pa_internal.h"
 #include "prefill_kernel.cuh"
 #include "prefix_kernel.cuh"
@@ -167,7 +168,7 @@ struct DecodeReq {
   cudaStream_t stream;
 };
 
-pa_status_t validate_and_pick(const DecodeReq& r, DecodeInstance* inst) {
+pa_status_t validate_request(const DecodeReq& r) {
   if (r.num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs < 0");
   if (r.q == nullptr || r.k_pool == nullptr || r.v_pool == nullptr || r.block_tables == nullptr ||
       r.context_lens == nullptr || r.out == nullptr)
@@ -186,6 +187,12 @@ pa_status_t validate_and_pick(const DecodeReq& r, DecodeInstance* inst) {
     return fail(PA_ERR_INVALID_ARG, "num_blocks * num_kv_heads * block_size must be < 2^31");
   if (static_cast<int64_t>(r.max_blocks_per_seq) * r.block_size >= (int64_t(1) << 31))
     return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq * block_size must be < 2^31");
+  return PA_OK;
+}
+
+pa_status_t validate_and_pick(const DecodeReq& r, DecodeInstance* inst) {
+  const pa_status_t st = validate_request(r);
+  if (st != PA_OK) return st;
   const int group = r.num_q_heads / r.num_kv_heads;
   bool found = false;
   // bf16 runs on tensor cores for every group size, MHA included: measured on
@@ -359,6 +366,8 @@ struct SplitExtras {
   int pmax = 0;
   bool after_prefix_kernel = false;  // launched right after the prefix kernel
   int window = 0;                    // sliding window (0 = none)
+  bool sinks = false;                // the first num_sinks tokens stay visible beside it
+  int num_sinks = 0;
 };
 
 // Which split-decode kernel runs. Measured on B200 (bf16, head_dim 128):
@@ -382,6 +391,28 @@ bool use_stream_kernel(const DecodeReq& r, bool suffix_pass) {
          static_cast<int64_t>(r.max_blocks_per_seq) * r.block_size >= kDeepContextTokens;
 }
 
+// The merge grid is a programmatic dependent of the decode grid: it may be
+// scheduled before the decode grid ends and waits on the device
+// (griddepcontrol.wait) until the partials are complete and visible.
+pa_status_t launch_merge(const void* merge, const DecodeReq& r, DecodeArgs& a) {
+  int bs = r.block_size;
+  void* margs[] = {&a, &bs};
+  cudaLaunchConfig_t cfg{};
+  const int64_t merge_rows = static_cast<int64_t>(r.num_seqs) * r.num_q_heads;
+  cfg.gridDim = dim3(static_cast<unsigned>((merge_rows + kMergeRowsPerCta - 1) / kMergeRowsPerCta));
+  cfg.blockDim = dim3(32 * kMergeRowsPerCta);
+  cfg.dynamicSmemBytes = 0;
+  cfg.stream = r.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelExC(&cfg, merge, margs);
+  if (err != cudaSuccess) return fail(PA_ERR_CUDA, "merge launch: %s", cudaGetErrorString(err));
+  return PA_OK;
+}
+
 // clear_header: zero the workspace's control header on r.stream right before
 // the launch, after every host-side check has passed (a refused call leaves
 // the workspace untouched).
@@ -395,7 +426,7 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
   st = host_validate(r);
   if (st != PA_OK) return st;
 
-  DecodeArgs a{};
+  SinksArgs a{};  // the kernels without sinks take its DecodeArgs part
   a.q = r.q;
   a.out = r.out;
   a.block_tables = r.block_tables;
@@ -426,6 +457,7 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
                                  r.max_blocks_per_seq, partition_tokens);
     if (extras != nullptr && extras->window > 0) {
       a.window = extras->window;
+      a.num_sinks = extras->num_sinks;
     } else if (extras != nullptr) {
       L.seg_off = extras->seg_off;
       L.m_off = extras->m_off;
@@ -451,7 +483,8 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
     if (st != PA_OK) return st;
     int occ = 0;
     const bool suffix_pass = a.seq_skip_blocks != nullptr;
-    if (use_stream_kernel(r, suffix_pass)) {
+    const bool sinks = extras != nullptr && extras->sinks;
+    if (sinks || use_stream_kernel(r, suffix_pass)) {
       // Balanced pieces per warp (paged_decode_stream_kernel). At most this
       // many pieces per (sequence, KV head): the slots after the prefix
       // pass's (none outside shared-prefix decode).
@@ -459,11 +492,12 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
       const int pb = partition_tokens / r.block_size;
       a.max_pieces = (r.max_blocks_per_seq + pb - 1) / pb + 1;
       // Units of one KV head's list, at most: bounds the grid for small batches.
+      // (with sinks a sequence may list one unit twice)
       const int64_t units_max = static_cast<int64_t>(r.num_seqs) *
-                                ((static_cast<int64_t>(r.max_blocks_per_seq) * r.block_size + 15) / 16);
+                                ((static_cast<int64_t>(r.max_blocks_per_seq) * r.block_size + 15) / 16 + (sinks ? 1 : 0));
       if (units_max >= (int64_t(1) << 31))
         return fail(PA_ERR_UNSUPPORTED, "num_seqs * max context / 16 must be < 2^31");
-      const DecodeInstance::Stream& sk = inst.stream[suffix_pass ? 1 : 0];
+      const DecodeInstance::Stream& sk = sinks ? inst.sinks : inst.stream[suffix_pass ? 1 : 0];
       kernel = sk.kernel;
       threads = sk.threads;
       smem = sk.fixed_smem + (2 * r.num_seqs + 1) * 4;
@@ -530,26 +564,90 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
   }
   if (err != cudaSuccess) return fail(PA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(err));
   if (split) {
-    // The merge grid is a programmatic dependent of the decode grid: it may be
-    // scheduled before the decode grid ends and waits on the device
-    // (griddepcontrol.wait) until the partials are complete and visible.
-    int bs = r.block_size;
-    void* margs[] = {&a, &bs};
-    cudaLaunchConfig_t cfg{};
-    const int64_t merge_rows = static_cast<int64_t>(r.num_seqs) * r.num_q_heads;
-    cfg.gridDim = dim3(static_cast<unsigned>((merge_rows + kMergeRowsPerCta - 1) / kMergeRowsPerCta));
-    cfg.blockDim = dim3(32 * kMergeRowsPerCta);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = r.stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelExC(&cfg, inst.merge, margs);
-    if (err != cudaSuccess) return fail(PA_ERR_CUDA, "merge launch: %s", cudaGetErrorString(err));
+    st = launch_merge(inst.merge, r, a);
+    if (st != PA_OK) return st;
   }
   return launch_error("decode");
+}
+
+// ---- decode over the 4-bit cache ----------------------------------------------------------
+pa_status_t run_decode_q4(const DecodeReq& r, int window, int num_sinks, int partition_tokens, void* workspace,
+                          size_t workspace_bytes) {
+  pa_status_t st = validate_request(r);
+  if (st != PA_OK) return st;
+  if (window < 0 || num_sinks < 0) return fail(PA_ERR_INVALID_ARG, "window and num_sinks must be >= 0");
+  if (r.dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "pa_decode_q4 takes bf16 queries");
+  DecodeInstance inst;
+  const int group = r.num_q_heads / r.num_kv_heads;
+  if (group > 16 || !find_decode_q4(r.head_dim, r.block_size, &inst))
+    return fail(PA_ERR_UNSUPPORTED, "no 4-bit kernel for head_dim=%d block_size=%d group=%d", r.head_dim,
+                r.block_size, group);
+  if (partition_tokens <= 0 || partition_tokens % r.block_size != 0)
+    return fail(PA_ERR_INVALID_ARG, "partition_tokens (%d) must be a positive multiple of block_size",
+                partition_tokens);
+  if (r.num_seqs > kMaxSplitSeqs)
+    return fail(PA_ERR_UNSUPPORTED, "pa_decode_q4 takes at most %d sequences", kMaxSplitSeqs);
+  if (r.num_seqs == 0) return ok();
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(PA_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+  const SplitLayout L = split_layout(r.num_seqs, r.num_q_heads, r.head_dim, r.block_size, r.max_blocks_per_seq,
+                                     partition_tokens);
+  if (workspace_bytes < L.total)
+    return fail(PA_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", workspace_bytes, L.total);
+  // Units of one list, at most: bounds the grid for small batches (with sinks
+  // a sequence may list one unit twice).
+  const int64_t units_max = static_cast<int64_t>(r.num_seqs) *
+                            ((static_cast<int64_t>(r.max_blocks_per_seq) * r.block_size + 15) / 16 + 1);
+  if (units_max >= (int64_t(1) << 31))
+    return fail(PA_ERR_UNSUPPORTED, "num_seqs * max context / 16 must be < 2^31");
+
+  SinksArgs a{};
+  a.q = r.q;
+  a.out = r.out;
+  a.block_tables = r.block_tables;
+  a.context_lens = r.context_lens;
+  a.dev_err = r.dev_err;
+  a.num_seqs = r.num_seqs;
+  a.num_q_heads = r.num_q_heads;
+  a.num_kv_heads = r.num_kv_heads;
+  a.group = group;
+  a.num_blocks = r.num_blocks;
+  a.max_blocks_per_seq = r.max_blocks_per_seq;
+  a.scale_log2 = r.scale * 1.4426950408889634f;
+  a.l2_hint = l2_hint_default();
+  a.window = window;
+  a.num_sinks = window > 0 ? num_sinks : 0;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.seg_pieces = reinterpret_cast<int32_t*>(ws + L.seg_off);
+  a.part_m = reinterpret_cast<float*>(ws + L.m_off);
+  a.part_l = reinterpret_cast<float*>(ws + L.l_off);
+  a.part_acc = reinterpret_cast<float*>(ws + L.acc_off);
+  a.partition_blocks = partition_tokens / r.block_size;
+  a.max_partitions = L.pmax;
+  a.max_pieces = L.pmax;
+  a.persistent = 1;
+
+  DeviceInfo dinfo;
+  st = device_info(&dinfo);
+  if (st != PA_OK) return st;
+  const int smem = inst.fixed_smem + (2 * r.num_seqs + 1) * 4;
+  st = prepare_kernel(inst.kernel, smem);
+  if (st != PA_OK) return st;
+  int occ = 0;
+  st = occupancy(inst.kernel, inst.threads, smem, &occ);
+  if (st != PA_OK) return st;
+  int q_tiles = (group + 7) / 8;
+  const int64_t W = inst.threads / 32, lists = static_cast<int64_t>(r.num_kv_heads) * q_tiles;
+  const int64_t need = (units_max * lists + W - 1) / W, at_least = (lists + W - 1) / W;
+  const int64_t ctas = std::max(at_least, std::min<int64_t>(need, static_cast<int64_t>(dinfo.sms) * occ));
+  const void *kp = r.k_pool, *vp = r.v_pool;
+  void* args[] = {&kp, &vp, &q_tiles, &a};
+  const cudaError_t err = cudaLaunchKernel(inst.kernel, dim3(static_cast<unsigned>(ctas)), dim3(inst.threads), args,
+                                           smem, r.stream);
+  if (err != cudaSuccess) return fail(PA_ERR_CUDA, "decode_q4 launch: %s", cudaGetErrorString(err));
+  st = launch_merge(inst.merge, r, a);
+  if (st != PA_OK) return st;
+  return launch_error("decode_q4");
 }
 
 // ---- uploads of host-built plans --------------------------------------------------------
@@ -1625,6 +1723,39 @@ pa_status_t pa_decode_split_window(const void* q, const void* k_pool, const void
   SplitExtras ex;
   ex.window = window;
   return run_decode(r, true, partition_tokens, workspace, workspace_bytes, &ex);
+}
+
+pa_status_t pa_decode_split_sinks(const void* q, const void* k_pool, const void* v_pool,
+                                  const int32_t* block_tables, const int32_t* context_lens,
+                                  int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                  int block_size, int num_blocks, int max_blocks_per_seq,
+                                  float scale, pa_dtype_t dtype, int partition_tokens, int window,
+                                  int num_sinks, void* workspace, size_t workspace_bytes, void* out,
+                                  uint32_t* dev_err, void* stream) {
+  PA_NVTX_RANGE("pa_decode_split_sinks");
+  if (window < 1) return fail(PA_ERR_INVALID_ARG, "window must be >= 1");
+  if (num_sinks < 0) return fail(PA_ERR_INVALID_ARG, "num_sinks must be >= 0");
+  DecodeReq r{q, k_pool, v_pool, block_tables, context_lens, num_seqs, num_q_heads, num_kv_heads,
+              head_dim, block_size, num_blocks, max_blocks_per_seq, scale, dtype, out, dev_err,
+              static_cast<cudaStream_t>(stream)};
+  SplitExtras ex;
+  ex.window = window;
+  ex.sinks = true;
+  ex.num_sinks = num_sinks;
+  return run_decode(r, true, partition_tokens, workspace, workspace_bytes, &ex);
+}
+
+pa_status_t pa_decode_q4(const void* q, const void* k_pool, const void* v_pool,
+                         const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                         int num_blocks, int max_blocks_per_seq, float scale, pa_dtype_t dtype,
+                         int window, int num_sinks, int partition_tokens, void* workspace,
+                         size_t workspace_bytes, void* out, uint32_t* dev_err, void* stream) {
+  PA_NVTX_RANGE("pa_decode_q4");
+  DecodeReq r{q, k_pool, v_pool, block_tables, context_lens, num_seqs, num_q_heads, num_kv_heads,
+              head_dim, block_size, num_blocks, max_blocks_per_seq, scale, dtype, out, dev_err,
+              static_cast<cudaStream_t>(stream)};
+  return run_decode_q4(r, window, num_sinks, partition_tokens, workspace, workspace_bytes);
 }
 
 size_t pa_prefill_workspace_size(int num_seqs, int total_q, int num_q_heads, int num_kv_heads,

@@ -22,13 +22,16 @@ struct DecodeInstance {
     int threads = 0;
     int fixed_smem = 0;          // dynamic smem bytes before the per-sequence arrays
     int warps = 0;
-  } stream[2];
+  } stream[2], sinks;            // sinks: shape [0] built for a window with sinks
 };
 
 // Each returns false when (head_dim, block_size, group) has no instance.
 bool find_decode_f32(int head_dim, int block_size, int group, DecodeInstance* out);
 // deep: the CTA shape for long contexts (see decode_inst_bf16.cu).
 bool find_decode_bf16_mma(int head_dim, int block_size, bool deep, DecodeInstance* out);
+// 4-bit cache (bf16 queries): kernel, merge, threads, fixed_smem (before the
+// per-sequence arrays) and the warps in threads / 32.
+bool find_decode_q4(int head_dim, int block_size, DecodeInstance* out);
 
 struct PrefixInstance {
   const void* kernel = nullptr;  // prefix_decode_kernel<PrefixCfg<BS, D>> (or a prefill kernel)

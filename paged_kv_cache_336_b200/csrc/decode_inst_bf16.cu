@@ -13,6 +13,7 @@
 
 #include "decode_dispatch.h"
 #include "decode_kernel.cuh"
+#include "decode_sinks_kernel.cuh"
 #include "decode_stream_kernel.cuh"
 #include "prefill_kernel.cuh"
 #include "prefix_kernel.cuh"
@@ -31,6 +32,15 @@ static DecodeInstance make_bf16(const char* name) {
   r.stages = Cfg::NS;
   r.name = name;
   return r;
+}
+
+template <int BS, int D, int W, int NS>
+static void add_sinks(DecodeInstance* r) {
+  using Cfg = DecodeCfg<__nv_bfloat16, BS, D, 0, W, NS>;
+  r->sinks.kernel = reinterpret_cast<const void*>(&paged_decode_sinks_kernel<Cfg>);
+  r->sinks.threads = Cfg::kThreads;
+  r->sinks.fixed_smem = StreamCfg<Cfg>::kFixedSmem;
+  r->sinks.warps = Cfg::W;
 }
 
 template <int BS, int D, int W, int NS>
@@ -56,6 +66,8 @@ static void add_stream(DecodeInstance* r, int which) {
 template <int BS, int D>
 static void pick_stream(DecodeInstance* r) {
   const char* e = std::getenv("PAGEDKV_STREAM_SHAPE");
+  if constexpr (D == 256) add_sinks<BS, D, 4, 2>(r);
+  else add_sinks<BS, D, 8, 3>(r);
   if constexpr (D == 256) {
     add_stream<BS, D, 4, 2>(r, 0);
     add_stream<BS, D, 4, 2>(r, 1);

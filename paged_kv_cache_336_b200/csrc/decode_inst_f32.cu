@@ -1,6 +1,7 @@
 // fp32 instances of the paged decode kernel (CUDA-core path).
 #include "decode_dispatch.h"
 #include "decode_kernel.cuh"
+#include "decode_sinks_kernel.cuh"
 #include "decode_stream_kernel.cuh"
 
 namespace pagedkv {
@@ -21,6 +22,8 @@ static DecodeInstance make_f32() {
     st.fixed_smem = StreamCfg<Cfg>::kFixedSmem;
     st.warps = Cfg::W;
   }
+  r.sinks = r.stream[0];
+  r.sinks.kernel = reinterpret_cast<const void*>(&paged_decode_sinks_kernel<Cfg>);
   return r;
 }
 

@@ -1,0 +1,217 @@
+"""pa_decode_q4 against the 64-bit definition on the values that the pools stand
+for.
+
+Bound of an output element, with w_t the softmax weights, v = mid + s (c - 8):
+* p s is rounded to bf16, half a step of 2^-8: 2^-8 sum w s |c - 8|;
+* the output is rounded to bf16: 2^-8 |out|;
+* a logit's group sum starts at -128 Q and takes four products of codes up to
+  143 with q in fp32 accumulators, each off by at most a step (2^-23) of what
+  passes through them, less than 271 sum |q|: e = scale s 4 * 2^-23 * 271
+  sum |q|, doubled for the products' inner sums; a logit off by e moves an
+  output by at most 2 e sum w |v|;
+* exp2, the fp32 sums and the start value of O (which cancels at most 64 tokens
+  of 136 s p, against sum w s |c - 8|): 2^-18 of sum w (|v| + 16 s)."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import serving_ops as so
+from paged_kv_cache_336_b200 import binding
+
+pytestmark = pytest.mark.gpu
+
+
+def make(seed, lens, Hq, Hkv, D, bs, s_lo=0.1, s_hi=0.5, slack=1):
+    """Random 4-bit pools (scales up to s_hi, minima near -8 scales), shuffled tables."""
+    rng = np.random.default_rng(seed)
+    B, mbs = len(lens), max(1, max(-(-n // bs) for n in lens)) + slack
+    nb = sum(-(-n // bs) for n in lens) + 5
+    ids = rng.permutation(nb)
+    tables = np.full((B, mbs), -1, dtype=np.int32)
+    k = 0
+    for s, n in enumerate(lens):
+        for i in range(-(-n // bs)):
+            tables[s, i] = ids[k]
+            k += 1
+    pools = []
+    for _ in range(2):
+        pool = rng.integers(0, 256, (nb, Hkv, bs // 16, 9 * D), dtype=np.uint8)
+        sc = rng.uniform(s_lo, s_hi, (nb, Hkv, bs // 16, 16, D // 64))
+        mn = -7.5 * sc + rng.standard_normal(sc.shape) * s_hi
+        bits = np.stack([so.bf16_bits(sc), so.bf16_bits(mn)], -1)
+        pool[..., 8 * D:] = bits.reshape(*bits.shape[:3], -1).view(np.uint8)
+        pools.append(pool.reshape(nb, Hkv, -1))
+    q = torch.from_numpy(rng.standard_normal((B, Hq, D))).to(torch.bfloat16)
+    return q, pools[0], pools[1], tables, np.asarray(lens, dtype=np.int32)
+
+
+def dense(pool, D, bs, value):
+    """(values, s (c - 8), s) of a pool as [NB, Hkv, bs, D]."""
+    NB, H = pool.shape[:2]
+    sub = pool.reshape(NB, H, bs // 16, 9 * D)
+    codes = sub[..., :8 * D].reshape(NB, H, bs // 16, 16, D // 2)
+    nib = np.stack([codes & 15, codes >> 4], -1).reshape(NB, H, bs // 16, 16, D).astype(np.float64)
+    at = np.empty((16, D), dtype=np.int64)
+    for r in range(16):
+        for c in range(D // 8):
+            at[r, 8 * c:8 * c + 8] = 2 * so.q4_word_offset(r, c, D, value) + np.arange(8)
+    code = np.take_along_axis(nib, np.broadcast_to(at, nib.shape), -1)
+    pair = so.bf16_value(np.ascontiguousarray(sub[..., 8 * D:]).view(np.uint16))
+    pair = pair.reshape(NB, H, bs // 16, 16, D // 64, 2).astype(np.float64).repeat(64, -2)
+    flat = [x.reshape(NB, H, bs, D) for x in
+            (pair[..., 1] + pair[..., 0] * code, pair[..., 0] * (code - 8), pair[..., 0])]
+    return flat
+
+
+def test_dense_helper_is_the_oracles():
+    q, k, v, _, _ = make(1, [20], 1, 2, 128, 32)
+    for pool, value in ((k, False), (v, True)):
+        assert np.array_equal(dense(pool, 128, 32, value)[0], oracle.q4_dense(pool, 128, 32, value))
+
+
+def check(q, kp, vp, tables, lens, bs, window=0, sinks=0, partition_tokens=64, scale=None, out=None):
+    B, Hq, D = q.shape
+    scale = 1 / np.sqrt(D) if scale is None else scale
+    kd, _, ks = dense(kp, D, bs, False)
+    vd, vc, vs = dense(vp, D, bs, True)
+    q64 = q.double().numpy()
+
+    def attend(values):
+        return oracle.paged_decode_sinks(q64, kd, values, tables, lens, scale, window, sinks)
+
+    want = attend(vd)
+    # broadcast a bound on the logits over heads: scale * s * sum |q| per query head
+    e = 2 * abs(scale) * ks.max() * 4 * 2.0 ** -23 * 271 * np.abs(q64).sum(-1, keepdims=True)
+    tol = 2.0 ** -8 * (attend(np.abs(vc)) + np.abs(want)) + 2 * e * attend(np.abs(vd)) + \
+        2.0 ** -18 * attend(np.abs(vd) + 16 * vs)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = binding.decode_q4(q.cuda(), torch.from_numpy(kp).cuda(), torch.from_numpy(vp).cuda(),
+                            torch.from_numpy(tables).cuda(), torch.from_numpy(lens).cuda(), scale,
+                            window=window, sinks=sinks, partition_tokens=partition_tokens, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    g = got.double().cpu().numpy()
+    assert np.all(np.isfinite(g))
+    bad = np.abs(g - want) - tol
+    assert np.all(bad <= 0), (float(bad.max()), np.unravel_index(bad.argmax(), bad.shape))
+    return got
+
+
+LENS = [0, 1, 15, 16, 17, 63, 64, 65, 200, 129]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bs", [16, 32])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 2), (8, 1), (12, 2), (16, 1), (18, 2)])
+def test_matches_definition(D, bs, Hq, Hkv):
+    check(*make(D + bs + Hq, LENS, Hq, Hkv, D, bs), bs)
+
+
+@pytest.mark.parametrize("D,bs", [(64, 32), (128, 16), (256, 16)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (17, 4), (40, 0), (64, 16), (70, 37), (33, 150),
+                                          (5000, 4)])
+def test_windows_and_sinks(D, bs, window, sinks):
+    q, k, v, tables, lens = make(window + sinks, LENS, 8, 2, D, bs)
+    hidden = tables.copy()                # blocks without a visible token are released
+    if window:
+        for s, n in enumerate(lens):
+            for b in range(tables.shape[1]):
+                t = np.arange(b * bs, min((b + 1) * bs, n))
+                if not ((t >= n - window) | (t < sinks)).any():
+                    hidden[s, b] = -1
+    check(q, k, v, hidden, lens, bs, window, sinks)
+
+
+@pytest.mark.parametrize("partition_tokens", [32, 512])
+def test_many_pieces(partition_tokens):
+    check(*make(5, [5000, 17, 2999, 0, 1024], 8, 2, 128, 16), 16, partition_tokens=partition_tokens)
+
+
+def test_one_long_sequence():
+    check(*make(6, [20001], 4, 1, 128, 16), 16, partition_tokens=512)
+
+
+def test_many_short_sequences():
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 40, 700).tolist()
+    check(*make(7, lens, 2, 1, 64, 16), 16)
+
+
+def test_negative_scale_and_tiny_and_large_steps():
+    check(*make(9, LENS, 4, 2, 128, 16), 16, scale=-0.2)
+    check(*make(10, LENS, 4, 2, 128, 16, s_lo=1e-20, s_hi=1e-19), 16)
+    q, k, v, tables, lens = make(11, LENS, 4, 2, 64, 16, s_lo=2.0 ** 60, s_hi=2.0 ** 61)
+    check(q, k, v, tables, lens, 16, scale=2.0 ** -64)
+
+
+def test_rows_that_are_not_visible_may_hold_anything():
+    """All-ones bytes (codes 15, scale and minimum NaN) wherever nothing is visible."""
+    bs, D, window, sinks = 32, 128, 21, 5
+    q, k, v, tables, lens = make(12, [200, 31, 22, 1, 100], 8, 2, D, bs)
+    want = check(q, k, v, tables, lens, bs, window, sinks)
+    see = np.zeros((k.shape[0], bs), dtype=bool)
+    for s, n in enumerate(lens):
+        for t in range(n):
+            if t >= n - window or t < sinks:
+                see[tables[s, t // bs], t % bs] = True
+    for pool in (k, v):
+        sub = pool.reshape(pool.shape[0], 2, bs // 16, 9 * D)
+        for b in range(pool.shape[0]):
+            for t in range(bs):
+                if not see[b, t]:
+                    r = t % 16
+                    sub[b, :, t // 16, r * D // 2:(r + 1) * D // 2] = 0xff
+                    sub[b, :, t // 16, 8 * D + r * D // 16:8 * D + (r + 1) * D // 16] = 0xff
+    got = binding.decode_q4(q.cuda(), torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(),
+                            torch.from_numpy(tables).cuda(), torch.from_numpy(lens).cuda(),
+                            1 / np.sqrt(D), window=window, sinks=sinks, partition_tokens=64)
+    assert torch.equal(got, want)
+
+
+def test_a_nan_that_is_visible_reaches_the_output():
+    q, k, v, tables, lens = make(13, [40, 40], 2, 1, 64, 16)
+    at = v.reshape(v.shape[0], 1, 9 * 64)[tables[0, 1], 0]
+    at[512 + 4 * 3:512 + 4 * 3 + 4] = 0xff
+    args = [torch.from_numpy(x).cuda() for x in (k, v, tables, lens)]
+    got = binding.decode_q4(q.cuda(), *args, 0.1)
+    assert torch.isnan(got[0]).all() and torch.isfinite(got[1]).all()
+
+
+def test_bad_blocks_and_lengths_are_reported():
+    q, k, v, tables, lens = make(14, [40, 50, 20], 4, 2, 64, 16)
+    args = [torch.from_numpy(x).cuda() for x in (k, v, tables, lens)]
+    want = binding.decode_q4(q.cuda(), *args, 0.1)
+    tables[0, 1] = k.shape[0]
+    lens[2] = 16 * tables.shape[1] + 1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = [torch.from_numpy(x).cuda() for x in (k, v, tables, lens)]
+    got = binding.decode_q4(q.cuda(), *args, 0.1, dev_err=err)
+    assert int(err.item()) == binding.DEVERR_BLOCK_ID | binding.DEVERR_CONTEXT_LEN
+    assert torch.equal(got[1], want[1]) and torch.all(got[2] == 0)
+    assert not torch.equal(got[0], want[0]) and torch.isfinite(got[0]).all()
+
+
+def test_workspace_is_reused_and_results_repeat():
+    """Bit-equal results from one workspace over different batches, from a
+    captured graph, and with a dirty workspace."""
+    q, k, v, tables, lens = make(15, [3000, 17, 0, 500], 8, 2, 128, 16)
+    args = [torch.from_numpy(x).cuda() for x in (k, v, tables, lens)]
+    q = q.cuda()
+    ws = binding.SplitWorkspace(4, 8, 128, 16, tables.shape[1], 64)
+    a = binding.decode_q4(q, *args, 0.1, workspace=ws)
+    binding.decode_q4(q, *args, 0.3, window=30, sinks=3, workspace=ws)
+    ws.buffer[512:].fill_(0xff)
+    b = binding.decode_q4(q, *args, 0.1, workspace=ws)
+    assert torch.equal(a, b)
+    out = torch.empty_like(a)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        binding.decode_q4(q, *args, 0.1, workspace=ws, out=out)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, a)

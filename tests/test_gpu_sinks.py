@@ -1,0 +1,85 @@
+"""pa_decode_split_sinks against the oracle's visible-token definition: sinks
+that end before, inside and past the window, released blocks, fp32 and bf16,
+every head_dim, few and many pieces."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from paged_kv_cache_336_b200 import binding, workloads
+
+from gpu_util import check_close, device_tables, setup, to_f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,G,bs,D", [
+    (workloads.F32, 1, 16, 128), (workloads.F32, 2, 32, 64), (workloads.BF16, 1, 32, 128),
+    (workloads.BF16, 8, 16, 128), (workloads.BF16, 6, 16, 64), (workloads.BF16, 16, 32, 256)])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (7, 4), (40, 16), (40, 17), (16, 37), (97, 0),
+                                          (33, 150), (30, 5000), (10_000, 4)])
+def test_matches_oracle(dtype, G, bs, D, window, sinks):
+    w = workloads.random_small(40 + G + bs, num_seqs=8, num_q_heads=2 * G, num_kv_heads=2,
+                               head_dim=D, block_size=bs, dtype=dtype, max_ctx=12 * bs,
+                               fixed_lens=[0, 1, 12 * bs, bs + 1, window + 1 if window < 150 else 2])
+    bm, k_pool, v_pool = setup(w)
+    q = workloads.draw_queries(w, 8, device="cuda")
+    bt, ctx, tables, ctx_np = device_tables(bm, list(range(8)))
+    want = oracle.paged_decode_sinks(to_f64(q), to_f64(k_pool), to_f64(v_pool), tables, ctx_np,
+                                     w.scale, window, sinks)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, window, sinks,
+                                     partition_tokens=2 * bs, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check_close(to_f64(out), want, dtype, f"window {window} sinks {sinks}")
+    # blocks that hold neither a sink nor a token of the window are never read
+    hidden = bt.clone()
+    for s in range(8):
+        for b in range(bt.shape[1]):
+            t = np.arange(b * bs, min((b + 1) * bs, int(ctx_np[s])))
+            if not ((t >= int(ctx_np[s]) - window) | (t < sinks)).any():
+                hidden[s, b] = -1
+    again = binding.decode_split_sinks(q, k_pool, v_pool, hidden, ctx, w.scale, window, sinks,
+                                       partition_tokens=2 * bs, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(out, again)
+    if sinks == 0:
+        ref = binding.decode_split_window(q, k_pool, v_pool, bt, ctx, w.scale, window, partition_tokens=2 * bs)
+        check_close(to_f64(ref), to_f64(out), dtype, "no sinks is the window")
+
+
+def test_rows_outside_what_is_visible_may_hold_anything():
+    """NaN everywhere but in the visible tokens."""
+    bs, window, sinks = 16, 21, 5
+    w = workloads.random_small(77, num_seqs=4, num_q_heads=8, num_kv_heads=2, head_dim=128,
+                               block_size=bs, dtype=workloads.BF16, max_ctx=200,
+                               fixed_lens=[200, 31, 22, 100])
+    bm, k_pool, v_pool = setup(w)
+    q = workloads.draw_queries(w, 4, device="cuda")
+    bt, ctx, tables, ctx_np = device_tables(bm, list(range(4)))
+    want = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, window, sinks)
+    see = torch.zeros(k_pool.shape[0], bs, dtype=torch.bool)
+    for s in range(4):
+        for t in range(int(ctx_np[s])):
+            if t >= int(ctx_np[s]) - window or t < sinks:
+                see[int(tables[s, t // bs]), t % bs] = True
+    hide = ~see.cuda()[:, None, :, None].expand_as(k_pool)
+    k_pool[hide] = float("nan")
+    v_pool[hide] = float("nan")
+    got = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, window, sinks)
+    assert torch.equal(got, want)
+
+
+def test_long_contexts_many_pieces():
+    w = workloads.random_small(6, num_seqs=3, num_q_heads=8, num_kv_heads=2, head_dim=128,
+                               block_size=16, dtype=workloads.BF16, max_ctx=40000,
+                               fixed_lens=[40000, 33333, 900])
+    bm, k_pool, v_pool = setup(w)
+    q = workloads.draw_queries(w, 3, device="cuda")
+    bt, ctx, tables, ctx_np = device_tables(bm, [0, 1, 2])
+    want = oracle.paged_decode_sinks(to_f64(q), to_f64(k_pool), to_f64(v_pool), tables, ctx_np,
+                                     w.scale, 9000, 1000)
+    got = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, 9000, 1000)
+    check_close(to_f64(got), want, workloads.BF16, "long")
