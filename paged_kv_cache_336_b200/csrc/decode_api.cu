@@ -570,6 +570,24 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
   return launch_error("decode");
 }
 
+// The 4-bit kernel's warps trade registers up to what the block was launched
+// with; fewer than it counts on would leave them waiting, so that is looked at
+// once per kernel.
+pa_status_t check_launch_regs(const void* kernel, int regs) {
+  static std::mutex mu;
+  static std::vector<const void*> done;
+  std::lock_guard<std::mutex> lock(mu);
+  for (const void* k : done)
+    if (k == kernel) return PA_OK;
+  cudaFuncAttributes at{};
+  const cudaError_t err = cudaFuncGetAttributes(&at, kernel);
+  if (err != cudaSuccess) return fail(PA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(err));
+  if (at.numRegs != regs)
+    return fail(PA_ERR_UNSUPPORTED, "the 4-bit kernel was built with %d registers a thread, not %d", at.numRegs, regs);
+  done.push_back(kernel);
+  return PA_OK;
+}
+
 // ---- decode over the 4-bit cache ----------------------------------------------------------
 pa_status_t run_decode_q4(const DecodeReq& r, int window, int num_sinks, int partition_tokens, void* workspace,
                           size_t workspace_bytes) {
@@ -630,6 +648,8 @@ pa_status_t run_decode_q4(const DecodeReq& r, int window, int num_sinks, int par
   DeviceInfo dinfo;
   st = device_info(&dinfo);
   if (st != PA_OK) return st;
+  st = check_launch_regs(inst.kernel, inst.launch_regs);
+  if (st != PA_OK) return st;
   const int smem = inst.fixed_smem + (2 * r.num_seqs + 1) * 4;
   st = prepare_kernel(inst.kernel, smem);
   if (st != PA_OK) return st;
@@ -637,7 +657,7 @@ pa_status_t run_decode_q4(const DecodeReq& r, int window, int num_sinks, int par
   st = occupancy(inst.kernel, inst.threads, smem, &occ);
   if (st != PA_OK) return st;
   int q_tiles = (group + 7) / 8;
-  const int64_t W = inst.threads / 32, lists = static_cast<int64_t>(r.num_kv_heads) * q_tiles;
+  const int64_t W = inst.warps, lists = static_cast<int64_t>(r.num_kv_heads) * q_tiles;
   const int64_t need = (units_max * lists + W - 1) / W, at_least = (lists + W - 1) / W;
   const int64_t ctas = std::max(at_least, std::min<int64_t>(need, static_cast<int64_t>(dinfo.sms) * occ));
   const void *kp = r.k_pool, *vp = r.v_pool;

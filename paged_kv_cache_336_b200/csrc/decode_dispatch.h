@@ -13,6 +13,8 @@ struct DecodeInstance {
   int threads = 0;
   int fixed_smem = 0;            // dynamic smem bytes before the prefix array
   int stages = 0;
+  int warps = 0;                 // 4-bit decode: consumer warps
+  int launch_regs = 0;           // 4-bit decode: registers a thread that its split counts on
   const char* name = "";
   // Split decode: paged_decode_stream_kernel<Cfg> (balanced pieces per warp),
   // in two CTA shapes: [0] the long-context one, [1] a smaller one that
@@ -30,7 +32,7 @@ bool find_decode_f32(int head_dim, int block_size, int group, DecodeInstance* ou
 // deep: the CTA shape for long contexts (see decode_inst_bf16.cu).
 bool find_decode_bf16_mma(int head_dim, int block_size, bool deep, DecodeInstance* out);
 // 4-bit cache (bf16 queries): kernel, merge, threads, fixed_smem (before the
-// per-sequence arrays) and the warps in threads / 32.
+// per-sequence arrays), warps.
 bool find_decode_q4(int head_dim, int block_size, DecodeInstance* out);
 
 struct PrefixInstance {

@@ -1,4 +1,5 @@
 // Instances of the 4-bit decode kernel (bf16 queries, groups 1..16).
+#include <cstdlib>
 #include "decode_dispatch.h"
 #include "decode_q4_kernel.cuh"
 
@@ -13,15 +14,27 @@ static DecodeInstance make_q4() {
   r.threads = Cfg::kThreads;
   r.fixed_smem = Cfg::kFixedSmem;
   r.stages = Cfg::NS;
+  r.warps = Cfg::W;
+  r.launch_regs = Cfg::kLaunchRegs;
   r.name = "mma_q4";
   return r;
 }
 
 template <int BS>
 static bool pick(int head_dim, DecodeInstance* out) {
-  if (head_dim == 64) { *out = make_q4<BS, 64, 8, 4, 4>(); return true; }
-  if (head_dim == 128) { *out = make_q4<BS, 128, 8, 4, 2>(); return true; }
-  if (head_dim == 256) { *out = make_q4<BS, 256, 8, 2, 2>(); return true; }
+  if (head_dim == 64) { *out = make_q4<BS, 64, 12, 4, 4>(); return true; }
+  if (head_dim == 128) {
+    const char* e = std::getenv("Q4SHAPE");
+    const int v = e ? std::atoi(e) : 0;
+    if constexpr (BS == 16) {
+    if (v == 1) { *out = make_q4<BS, 128, 8, 4, 4>(); return true; }
+    if (v == 2) { *out = make_q4<BS, 128, 12, 3, 4>(); return true; }
+    if (v == 3) { *out = make_q4<BS, 128, 12, 3, 3>(); return true; }
+    if (v == 4) { *out = make_q4<BS, 128, 8, 4, 3>(); return true; }
+    if (v == 5) { *out = make_q4<BS, 128, 12, 2, 4>(); return true; }
+    }
+    *out = make_q4<BS, 128, 12, 4, 3>(); return true; }
+  if (head_dim == 256) { *out = make_q4<BS, 256, 8, 2, 4>(); return true; }
   return false;
 }
 

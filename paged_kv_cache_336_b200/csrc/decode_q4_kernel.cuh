@@ -36,23 +36,33 @@
 // about 0.9 mask, shift and permute instructions a value.
 #pragma once
 
+#include <climits>
+
 #include "decode_sinks_kernel.cuh"
 #include "q4_common.cuh"
 
 namespace pagedkv {
 
-// W warps; a stage holds US units (one softmax step); NS stages per warp.
+// W consumer warps and four producer warps; a step takes up to US units; each consumer's ring has NS slots of US sub-tiles, filled
+// in the order K, V, K, V, ... of its steps.
 template <int BS_, int D_, int W_, int US_, int NS_>
 struct Q4Cfg {
   static constexpr int BS = BS_, D = D_, W = W_, US = US_, NS = NS_;
   static constexpr int UPB = BS / 16;
   using Geo = Q4Geo<D>;
-  static constexpr int kThreads = 32 * W;
-  static constexpr int kStageBytes = US * 2 * Geo::kSubBytes;  // K units, then V units
-  static constexpr int kRingBytes = W * NS * kStageBytes;
-  static constexpr int kFixedSmem = 128 + kRingBytes + W * NS * 8;
-  static_assert(kRingBytes % 16 == 0 && US <= 4 && US * NS <= 32, "stage layout");
-  static_assert(kFixedSmem + (2 * 4096 + 1) * 4 <= 226 * 1024, "shared memory budget exceeded");
+  static constexpr int kThreads = 32 * (W + 4);
+  static constexpr int kSlotBytes = US * Geo::kSubBytes;
+  static constexpr int kRingBytes = W * NS * kSlotBytes;
+  // ring | full, empty barriers [W][NS] | units present per slot [W][NS]
+  static constexpr int kFixedSmem = 128 + kRingBytes + W * NS * (8 + 8 + 4);
+  // Registers a thread at launch, and after the split (what the producers
+  // give up is what the consumers take).
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+  static constexpr int kProducerRegs = W == 12 ? 32 : 40;
+  static constexpr int kConsumerRegs = (kLaunchRegs * (W + 4) - kProducerRegs * 4) / W / 8 * 8;
+  static_assert(W % 4 == 0 && W <= 12 && US <= 4 && NS >= 2 && NS <= 8, "whole warpgroups; ring layout");
+  static_assert(kConsumerRegs * W + kProducerRegs * 4 <= kLaunchRegs * (W + 4), "registers of the split");
+  static_assert(kRingBytes % 16 == 0 && kFixedSmem + (2 * 4096 + 1) * 4 <= 226 * 1024, "shared memory budget exceeded");
 };
 
 // Bulk copy global -> shared, completion on `bar`; addresses and size are
@@ -66,14 +76,19 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint3
       : "memory");
 }
 
-// D = A * B + C with D and C apart.
-__device__ __forceinline__ void mma_bf16_init(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                              const float (&c)[4]) {
+// D += A(16x16) * B(16x8), f16 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // 8x8 transpose of 16-bit elements across the warp (mma fragment layout).
@@ -83,21 +98,71 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   return r;
 }
 
-// Codes j (low half) and j + 4 (high half) of a word as bf16 128 + code.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) { return ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u; }
+// D = A * B (first) or D += A * B for bytes, A (16 x 32) unsigned, B (32 x 8)
+// signed or unsigned, 32-bit sums.
+#define PA_MMA_BYTES(types)                                                                          \
+  if (first)                                                                                         \
+    asm volatile("mma.sync.aligned.m16n8k32.row.col." types                                          \
+                 " {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"              \
+                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])                                    \
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));            \
+  else                                                                                               \
+    asm volatile("mma.sync.aligned.m16n8k32.row.col." types                                          \
+                 " {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"                  \
+                 : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])                                    \
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1))
+template <bool kSigned>
+__device__ __forceinline__ void mma_bytes(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool first) {
+  if constexpr (kSigned) {
+    PA_MMA_BYTES("s32.u8.s8.s32");
+  } else {
+    PA_MMA_BYTES("s32.u8.u8.s32");
+  }
+}
+#undef PA_MMA_BYTES
 
-// N consecutive 32-bit words of shared memory, N * 4 bytes aligned.
+// Greater of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The codes of a word less 8, as f16: out[j] holds those of dims j (low half) and
+// j + 4. A mask-or puts a code into the mantissa of 1024, from where it stands
+// (1024 + c, or 1024 + 16 c for the second nibble of a byte), and one packed
+// add or multiply-add makes c - 8 of it, exactly: 5 integer and 4 packed
+// instructions for 8 codes, on different pipes. The mask-or's constants come
+// from registers (an instruction takes one immediate at most).
+struct CodeBits {
+  uint32_t lo4, hi4, k1024;
+  __device__ __forceinline__ CodeBits() {
+    asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(lo4));
+    asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(hi4));
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
+  }
+  __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&out)[4]) const {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t x, y;
+      asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w >> (8 * b)), "r"(lo4), "r"(k1024));  // (a & b) | c
+      asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(w >> (8 * b)), "r"(hi4), "r"(k1024));
+      asm("add.rn.f16x2 %0, %1, %2;" : "=r"(out[2 * b]) : "r"(x), "r"(0xe408e408u));                   // - 1032
+      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(out[2 * b + 1]) : "r"(y), "r"(0x2c002c00u), "r"(0xd480d480u));  // / 16 - 72
+    }
+  }
+};
+
+// N consecutive 32-bit words at a shared-memory address, N * 4 bytes aligned.
 template <int N>
-__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
   if constexpr (N == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
   } else if constexpr (N == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x; w[1] = v.y;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
   } else {
     static_assert(N == 1, "1, 2 or 4 words");
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
   }
 }
 
@@ -109,196 +174,269 @@ struct Q4Warp {
   static constexpr int D = Cfg::D;
   static constexpr int US = Cfg::US;
   static constexpr int GR = Geo::kGroups;
+  // expo's range: scales up to 2^61; those below 2^-40 keep f16's 11 bits down
+  // to 2^-68, and pieces merged by 2^(m - M) stay within fp32's exponents.
+  static constexpr int kMinExpo = -40, kMaxExpo = 60;
 
-  uint32_t qb[GR][4][2];  // query operand
-  float nq[GR][2];        // -128 Q_i of heads 2t, 2t + 1
+  // Query operand: rint(2^k q), 16 bits, as high bytes (signed) and low bytes
+  // (unsigned) per octet of 8 dims that the lane holds (even dims, odd dims).
+  uint32_t qb[GR][2][2][2];
+  float qs[GR][2];        // 2^k Q_i of heads 2t, 2t + 1
+  float f[2];             // |scale| log2(e) 2^-k of heads 2t, 2t + 1
   float o[GR][4][4];      // O^T: dims 64 i + 8 g + 2 j (+ 1 for e >= 2), head 2t + (e & 1)
   float mid[GR][2];       // sum p (mn + 8 s) over this lane's tokens
-  float m[2], l[2];       // running max (log2 domain), this lane's part of the sum
-  float scale_log2;
+  // Softmax weights are held as 2^(y - m), m = top + expo - 14, with top the
+  // running maximum of the logits y (log2 domain) and 2^expo the largest power
+  // of two of the value scales met: then a weight times a scale is below 2^15
+  // and fits f16 with 39 binades to spare below.
+  float top[2], m[2], l[2];  // l: this lane's part of the sum
+  int expo;
+  // This lane's places in a sub-tile. K: its row (rows g and g + 8 of S are
+  // tokens tok and tok + 8); V: tokens t and 7 - t (+ 8); both: parameters.
+  CodeBits bits;
+  int tok;
+  uint32_t k_at, v_at[2], par_at;
 
-  __device__ __forceinline__ void begin(const __nv_bfloat16* row, bool valid, float scale, int lane) {
+  __device__ __forceinline__ void places(int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    tok = (g & 1) ? 7 - (g >> 1) : (g >> 1);
+    k_at = tok * Geo::kRowBytes + (D == 256 ? (tok & 1) * 64 + t * 16 : t * (8 * GR));
+    par_at = Geo::kCodeBytes + tok * Geo::kParamRow;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int tk = r ? 7 - t : t;
+      v_at[r] = tk * Geo::kRowBytes + ((g ^ Geo::v_turn(tk)) * (D / 16));
+    }
+  }
+
+  __device__ __forceinline__ void begin(const __nv_bfloat16* row, bool valid, float scale_log2, int lane) {
     const int t = lane & 3;
+    uint4 x[GR][2];
+    float largest = 0.f;
+#pragma unroll
+    for (int i = 0; i < GR; ++i) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        x[i][w] = make_uint4(0u, 0u, 0u, 0u);
+        if (valid) x[i][w] = *reinterpret_cast<const uint4*>(row + 64 * i + 16 * t + 8 * w);
+        const uint32_t v[4] = {x[i][w].x, x[i][w].y, x[i][w].z, x[i][w].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) largest = max_nan(largest, max_nan(fabsf(bf16_lo(v[j])), fabsf(bf16_hi(v[j]))));
+      }
+    }
+    largest = max_nan(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+    largest = max_nan(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+    // k brings the row's largest |q| into [2^14, 2^15); q of a negative scale is negated
+    const int e = max(static_cast<int>(__float_as_uint(largest) >> 23), 16);
+    const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);   // 2^k, k = 141 - e
+    const float down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);  // 2^-k
+    float fac = fabsf(scale_log2) * down;
+    if (!(largest < INFINITY)) fac = __uint_as_float(0x7fc00000u);
+    const float sgn = scale_log2 < 0.f ? -up : up;
 #pragma unroll
     for (int i = 0; i < GR; ++i) {
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (valid) x = *reinterpret_cast<const uint4*>(row + 64 * i + 16 * t + 8 * w);
-        qb[i][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);      // dims 0, 4
-        qb[i][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);      // dims 1, 5
-        qb[i][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);  // dims 2, 6
-        qb[i][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);  // dims 3, 7
-        sum += ((bf16_lo(x.x) + bf16_hi(x.x)) + (bf16_lo(x.y) + bf16_hi(x.y))) +
-               ((bf16_lo(x.z) + bf16_hi(x.z)) + (bf16_lo(x.w) + bf16_hi(x.w)));
+        const uint32_t v[4] = {x[i][w].x, x[i][w].y, x[i][w].z, x[i][w].w};
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd) {
+          uint32_t hi = 0, lo = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float q = (odd ? bf16_hi(v[j]) : bf16_lo(v[j])) * sgn;
+            sum += q;
+            const uint32_t n = static_cast<uint32_t>(__float2int_rn(q));
+            hi |= ((n >> 8) & 0xffu) << (8 * j);
+            lo |= (n & 0xffu) << (8 * j);
+          }
+          qb[i][w][0][odd] = hi;
+          qb[i][w][1][odd] = lo;
+        }
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      nq[i][0] = -128.f * __shfl_sync(0xffffffffu, sum, 8 * t);
-      nq[i][1] = -128.f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+      qs[i][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+      qs[i][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
       mid[i][0] = mid[i][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
     }
-    m[0] = m[1] = -INFINITY;
+    f[0] = __shfl_sync(0xffffffffu, fac, 8 * t);
+    f[1] = __shfl_sync(0xffffffffu, fac, 8 * t + 4);
+    top[0] = top[1] = m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
-    scale_log2 = scale;
+    expo = kMinExpo;
   }
 
-  // One step: the units u with bit u of `use` set (at least one). Token r of
-  // unit u takes part if lo[u] <= r < hi[u]; with kEdge false all do. Rows
-  // outside may hold anything, NaN parameters included.
-  template <bool kEdge>
-  __device__ __forceinline__ void step(const uint8_t* stage, uint32_t use, const int (&lo)[US], const int (&hi)[US],
-                                       int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    const int tok = (g & 1) ? 7 - (g >> 1) : (g >> 1);  // rows g and g + 8 of S: tokens tok, tok + 8
-    float x[US][4];
-    // ---- S = K Q^T -----------------------------------------------------------------
+  // A step is logits() and then attend(), over NU units whose sub-tiles lie one
+  // after the other at shared addresses k_tile and v_tile. kEdge (NU = 1): of
+  // the unit's rows tok and tok + 8 those with out[] set are not visible and
+  // may hold anything, NaN parameters included.
+  template <int NU, bool kEdge>
+  __device__ __forceinline__ void logits(uint32_t k_tile, float (&x)[NU][4], const bool (&out)[2]) const {
+    static_assert(!kEdge || NU == 1, "an edge step takes one unit");
+    const uint32_t k_row = k_tile + k_at, k_par = k_tile + par_at;
 #pragma unroll
-    for (int u = 0; u < US; ++u) {
-      if (kEdge && !(use >> u & 1)) {
-        x[u][0] = x[u][1] = x[u][2] = x[u][3] = -INFINITY;
-        continue;
-      }
-      const uint8_t* kt = stage + u * Geo::kSubBytes;
+    for (int u = 0; u < NU; ++u) {
       uint32_t w[2][2 * GR], par[2][GR];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const uint8_t* row = kt + (tok + 8 * r) * Geo::kRowBytes;
-        if constexpr (D == 256) {
+        const uint32_t at = k_row + u * Geo::kSubBytes + 8 * r * Geo::kRowBytes;
+        if constexpr (D == 256) {  // two halves of 64 bytes, swapped in odd rows
           uint32_t p0[4], p1[4];
-          lds_words(row + ((tok & 1) * 64) + t * 16, p0);
-          lds_words(row + ((tok & 1) ^ 1) * 64 + t * 16, p1);
+          lds_words(at, p0);
+          lds_words(at ^ 64u, p1);
 #pragma unroll
           for (int c = 0; c < 4; ++c) w[r][c] = p0[c], w[r][4 + c] = p1[c];
         } else {
-          lds_words(row + t * (8 * GR), w[r]);
+          lds_words(at, w[r]);
         }
-        lds_words(kt + Geo::kCodeBytes + (tok + 8 * r) * Geo::kParamRow, par[r]);
+        lds_words(k_par + u * Geo::kSubBytes + 8 * r * Geo::kParamRow, par[r]);
       }
-      x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
-        float s[4];
-        const float start[4] = {nq[i][0], nq[i][1], nq[i][0], nq[i][1]};
+        int sh[4], sl[4];
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          const uint32_t wa = w[0][2 * i + (ks >> 1)], wb = w[1][2 * i + (ks >> 1)];
-          const int j = 2 * (ks & 1);
-          const uint32_t a[4] = {code_pair(wa, j), code_pair(wb, j), code_pair(wa, j + 1), code_pair(wb, j + 1)};
-          if (ks == 0) mma_bf16_init(s, a, qb[i][ks][0], qb[i][ks][1], start);
-          else mma_bf16_16816(s, a, qb[i][ks][0], qb[i][ks][1]);
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t wa = w[0][2 * i + c], wb = w[1][2 * i + c];
+          constexpr uint32_t kNib = 0x0f0f0f0fu;
+          const uint32_t a[4] = {wa & kNib, wb & kNib, (wa >> 4) & kNib, (wb >> 4) & kNib};
+          mma_bytes<true>(sh, a, qb[i][c][0][0], qb[i][c][0][1], c == 0);
+          mma_bytes<false>(sl, a, qb[i][c][1][0], qb[i][c][1][1], c == 0);
         }
+        float s[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = __int2float_rn(256 * sh[e] + sl[e]);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float sc = bf16_lo(par[r][i]), mn = bf16_hi(par[r][i]) * -0.0078125f;  // mn Q = (-mn / 128) nq
-          x[u][2 * r] = fmaf(s[2 * r], sc, fmaf(mn, nq[i][0], x[u][2 * r]));
-          x[u][2 * r + 1] = fmaf(s[2 * r + 1], sc, fmaf(mn, nq[i][1], x[u][2 * r + 1]));
+          const float sc = bf16_lo(par[r][i]), mn = bf16_hi(par[r][i]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float base = i == 0 ? mn * qs[i][h] : fmaf(mn, qs[i][h], x[u][2 * r + h]);
+            x[u][2 * r + h] = fmaf(s[2 * r + h], sc, base);
+          }
         }
       }
+      if (kEdge) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[u][e] *= scale_log2;
-        if (kEdge) {
-          const int r = tok + 8 * (e >> 1);
-          if (r < lo[u] || r >= hi[u]) x[u][e] = -INFINITY;
-        }
+        for (int e = 0; e < 4; ++e) x[u][e] = out[e >> 1] ? -INFINITY : x[u][e] * f[e & 1];
       }
     }
+  }
+
+  template <int NU, bool kEdge>
+  __device__ __forceinline__ void attend(uint32_t v_tile, float (&x)[NU][4], const bool (&out)[2]) {
+    const uint32_t v_par = v_tile + par_at;
+    // ---- a value scale of 2^(expo + 1) or more asks for a larger expo (a NaN or an
+    // infinity only comes by here) ------------------------------------------------------
+    uint32_t smax = 0;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t par[GR];
+        lds_words(v_par + u * Geo::kSubBytes + 8 * r * Geo::kParamRow, par);
+#pragma unroll
+        for (int i = 0; i < GR; ++i) smax = __vmaxu2(smax, out[r] ? 0u : par[i]);
+      }
+    if (__any_sync(0xffffffffu, (smax & 0xffffu) >= static_cast<uint32_t>(expo + 128) << 7)) raise_expo<NU>(v_par, out);
     // ---- running softmax over the step's tokens ------------------------------------
-    float alpha[2];
+    float ref[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float mx = fmaxf(x[0][h], x[0][2 + h]);
 #pragma unroll
-      for (int u = 1; u < US; ++u) mx = fmaxf(mx, fmaxf(x[u][h], x[u][2 + h]));
+      for (int u = 1; u < NU; ++u) mx = fmaxf(mx, fmaxf(x[u][h], x[u][2 + h]));
 #pragma unroll
       for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      const float mn = fmaxf(m[h], mx);
-      alpha[h] = fast_exp2(m[h] - mn);
-      m[h] = mn;
-      l[h] *= alpha[h];
-#pragma unroll
-      for (int i = 0; i < GR; ++i) mid[i][h] *= alpha[h];
+      top[h] = fmaxf(top[h], kEdge ? mx : mx * f[h]);
+      ref[h] = top[h] + static_cast<float>(expo - 14);
     }
-    // ---- O^T += V^T P^T --------------------------------------------------------------
-    uint32_t pb[US][GR][2];
+    if (__any_sync(0xffffffffu, ref[0] != m[0] || ref[1] != m[1])) {  // (a NaN differs too)
 #pragma unroll
-    for (int u = 0; u < US; ++u) {
-      if (kEdge && !(use >> u & 1)) continue;
-      const uint8_t* vt = stage + (US + u) * Geo::kSubBytes;
+      for (int h = 0; h < 2; ++h) {
+        const float alpha = fast_exp2(m[h] - ref[h]);
+        m[h] = ref[h];
+        l[h] *= alpha;
+#pragma unroll
+        for (int i = 0; i < GR; ++i) {
+          mid[i][h] *= alpha;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[i][j][h] *= alpha;
+            o[i][j][2 + h] *= alpha;
+          }
+        }
+      }
+    }
+    uint32_t pb[NU][GR][2];  // P^T s, f16
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
       float p[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        p[e] = fast_exp2(x[u][e] - m[e & 1]);
+        p[e] = fast_exp2(kEdge ? x[u][e] - m[e & 1] : fmaf(x[u][e], f[e & 1], -m[e & 1]));
         l[e & 1] += p[e];
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         uint32_t par[GR];
-        lds_words(vt + Geo::kCodeBytes + (tok + 8 * r) * Geo::kParamRow, par);
-        const bool out = kEdge && (tok + 8 * r < lo[u] || tok + 8 * r >= hi[u]);
+        lds_words(v_par + u * Geo::kSubBytes + 8 * r * Geo::kParamRow, par);
 #pragma unroll
         for (int i = 0; i < GR; ++i) {
-          if (out) par[i] = 0u;
+          if (out[r]) par[i] = 0u;
           const float sc = bf16_lo(par[i]);
           const float mi = fmaf(8.f, sc, bf16_hi(par[i]));
-          pb[u][i][r] = movmatrix(pack_bf16x2(p[2 * r] * sc, p[2 * r + 1] * sc));
+          pb[u][i][r] = movmatrix(pack_f16x2(p[2 * r] * sc, p[2 * r + 1] * sc));
           mid[i][0] = fmaf(p[2 * r], mi, mid[i][0]);
           mid[i][1] = fmaf(p[2 * r + 1], mi, mid[i][1]);
         }
       }
     }
-    constexpr uint32_t kNeg136 = 0xc308c308u;
-    const uint32_t neg[4] = {kNeg136, kNeg136, kNeg136, kNeg136};
-    float start[GR][4];
+    // ---- O^T += V^T P^T --------------------------------------------------------------
 #pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      start[i][0] = start[i][1] = start[i][2] = start[i][3] = 0.f;
-#pragma unroll
-      for (int u = 0; u < US; ++u)
-        if (!kEdge || (use >> u & 1)) mma_bf16_16816(start[i], neg, pb[u][i][0], pb[u][i][1]);
-    }
-    float acc[GR][4][4];
-#pragma unroll
-    for (int i = 0; i < GR; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = start[i][e];
-#pragma unroll
-    for (int u = 0; u < US; ++u) {
-      if (kEdge && !(use >> u & 1)) continue;
-      const uint8_t* vt = stage + (US + u) * Geo::kSubBytes;
+    for (int u = 0; u < NU; ++u) {
       uint32_t w[4][GR];  // tokens t, 7 - t, 8 + t, 15 - t: k indices 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tk = (r & 1) ? 7 - t + 8 * (r >> 1) : t + 8 * (r >> 1);
-        lds_words(vt + tk * Geo::kRowBytes + ((g ^ Geo::v_turn(tk)) * (D / 16)), w[r]);
-      }
+      for (int r = 0; r < 4; ++r)
+        lds_words(v_tile + v_at[r & 1] + u * Geo::kSubBytes + (r >> 1) * 8 * Geo::kRowBytes, w[r]);
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < 2; ++half) {  // dims 8 g + 4 half + 0 .. 3
           const uint32_t sel = half ? 0x7632u : 0x5410u;
-          const uint32_t wa = __byte_perm(w[0][i], w[1][i], sel), wb = __byte_perm(w[2][i], w[3][i], sel);
+          uint32_t ca[4], cb[4];
+          bits.unpack(__byte_perm(w[0][i], w[1][i], sel), ca);
+          bits.unpack(__byte_perm(w[2][i], w[3][i], sel), cb);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t a[4] = {code_pair(wa, 2 * j), code_pair(wa, 2 * j + 1), code_pair(wb, 2 * j),
-                                   code_pair(wb, 2 * j + 1)};
-            mma_bf16_16816(acc[i][2 * half + j], a, pb[u][i][0], pb[u][i][1]);
+            const uint32_t a[4] = {ca[2 * j], ca[2 * j + 1], cb[2 * j], cb[2 * j + 1]};
+            mma_f16_16816(o[i][2 * half + j], a, pb[u][i][0], pb[u][i][1]);
           }
         }
       }
     }
+  }
+
+  // The largest exponent of the step's finite value scales becomes expo.
+  template <int NU>
+  __device__ __forceinline__ void raise_expo(uint32_t v_par, const bool (&out)[2]) {
+    uint32_t big = 0;
+#pragma unroll 1
+    for (int u = 0; u < NU; ++u)
 #pragma unroll
-    for (int i = 0; i < GR; ++i)
+      for (int r = 0; r < 2; ++r) {
+        uint32_t par[GR];
+        lds_words(v_par + u * Geo::kSubBytes + 8 * r * Geo::kParamRow, par);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][j][e] = fmaf(o[i][j][e], alpha[e & 1], acc[i][j][e]);
+        for (int i = 0; i < GR; ++i) {
+          const uint32_t e = (par[i] >> 7) & 0xffu;
+          if (!out[r] && e < 255u) big = max(big, e);
+        }
+      }
+    big = __reduce_max_sync(0xffffffffu, big);
+    expo = max(expo, min(static_cast<int>(big) - 127, kMaxExpo));
   }
 
   // Completes the sums over lanes; then head 2t + h's dims 64 i + 8 g + 0..7 are
@@ -340,127 +478,180 @@ struct Q4Warp {
   }
 };
 
-// q_tiles: runs of 8 query heads per KV head, ceil(group / 8).
+// What a warp has to do: units [g0, g1) of list (h, qt).
+struct Q4Run {
+  int g0, g1, gi, h, qt, C;
+};
+
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::kThreads, 1)
-    paged_decode_q4_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool, int q_tiles,
-                           const SinksArgs a) {
-  using Geo = typename Cfg::Geo;
-  constexpr int W = Cfg::W, NS = Cfg::NS, US = Cfg::US, BS = Cfg::BS, UPB = Cfg::UPB, D = Cfg::D;
-  constexpr uint32_t kUnitMask = (1u << US) - 1u;
-
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kRingBytes);
-  int* prefix = reinterpret_cast<int*>(bars + W * NS);  // [B + 1] units before sequence s
-  int* first_unit = prefix + a.num_seqs + 1;            // [B]
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int B = a.num_seqs;
-  const int max_tokens = a.max_blocks_per_seq * BS;
-  grid_dependents_launch();  // the merge grid may be scheduled; it waits for this grid before it reads
-  if (tid == 0) {
-    for (int i = 0; i < W * NS; ++i) mbar_init(&bars[i], 1);
-    fence_barrier_init();
-  }
-  const UnitLists lists = build_unit_lists<W>(a, BS, prefix, first_unit);
-
-  // ---- this warp's list and run of units -----------------------------------------------
+__device__ __forceinline__ Q4Run q4_run(const SinksArgs& a, const UnitLists& lists, int q_tiles, int warp) {
   const int num_lists = a.num_kv_heads * q_tiles;
-  const int wg = static_cast<int>(blockIdx.x) * W + warp;
-  const int groups = static_cast<int>(gridDim.x) * W / num_lists;
-  const int h = (wg % num_lists) / q_tiles, qt = wg % q_tiles;  // KV head, run of its query heads
-  const int gi = wg / num_lists;
-  const int C = max((lists.total + groups - 1) / groups, (lists.longest + a.max_pieces - 2) / (a.max_pieces - 1));
-  const int64_t g_begin = static_cast<int64_t>(gi) * C;
-  const int g0 = static_cast<int>(min(g_begin, static_cast<int64_t>(lists.total)));
-  const int g1 = static_cast<int>(min(g_begin + C, static_cast<int64_t>(lists.total)));
-  if (gi >= groups || g1 <= g0) return;
+  const int wg = static_cast<int>(blockIdx.x) * Cfg::W + warp;
+  const int groups = static_cast<int>(gridDim.x) * Cfg::W / num_lists;
+  Q4Run r;
+  r.h = (wg % num_lists) / q_tiles;  // KV head
+  r.qt = wg % q_tiles;               // run of its query heads
+  r.gi = wg / num_lists;
+  r.C = max((lists.total + groups - 1) / groups, (lists.longest + a.max_pieces - 2) / (a.max_pieces - 1));
+  const int64_t total = lists.total, begin = static_cast<int64_t>(r.gi) * r.C;
+  r.g0 = static_cast<int>(min(begin, total));
+  r.g1 = r.gi < groups ? static_cast<int>(min(begin + r.C, total)) : r.g0;
+  return r;
+}
 
-  auto locate = [&](int g) {  // last s with prefix[s] <= g
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (prefix[mid] <= g) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-  };
-  // Sub-tile of unit g of the list (>= 0), -1: nothing to read, -2: block id outside the pool.
-  auto unit_row = [&](int g) -> int {
-    if (g >= g1) return -1;
-    const int s = locate(g);
-    const int fu = first_unit[s];
-    if (fu < 0) return -1;
-    const int un = g - prefix[s], ns = sink_units(a, fu);
-    const int u = un < ns ? un : (fu & ~kSinkFlag) + un - ns;
-    const int phys = a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + u / UPB];
-    if (phys < 0 || phys >= a.num_blocks) return -2;
-    return (phys * a.num_kv_heads + h) * UPB + u % UPB;
-  };
+__device__ __forceinline__ int q4_locate(const int* prefix, int num_seqs, int g) {  // last s with prefix[s] <= g
+  int lo = 0, hi = num_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= g) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
 
+// Producer warp `which` of four fills the rings of consumers which, which + 4,
+// ...: eight lanes each, lane u of them its unit u. Block ids are read a step
+// ahead.
+template <class Cfg>
+__device__ __forceinline__ void q4_produce(const uint8_t* k_pool, const uint8_t* v_pool, const SinksArgs& a, int q_tiles,
+                                           const UnitLists& lists, const int* prefix, const int* first_unit,
+                                           uint8_t* ring, uint64_t* full, uint64_t* empty, uint32_t* present,
+                                           int which) {
+  using Geo = typename Cfg::Geo;
+  constexpr int US = Cfg::US, NS = Cfg::NS, UPB = Cfg::UPB;
+  const int lane = threadIdx.x & 31, u = lane & 7;
+  const int c = which + 4 * (lane >> 3);
+  Q4Run run = q4_run<Cfg>(a, lists, q_tiles, min(c, Cfg::W - 1));
+  if (c >= Cfg::W) run.g1 = run.g0;
+  const int g1 = run.g1, h = run.h;
+  ring += (min(c, Cfg::W - 1) * NS) * Cfg::kSlotBytes + u * Geo::kSubBytes;
+  full += min(c, Cfg::W - 1) * NS;
+  empty += min(c, Cfg::W - 1) * NS;
+  present += min(c, Cfg::W - 1) * NS;
   const uint64_t policy = l2_policy(a.l2_hint);
-  uint8_t* ring = smem + warp * NS * Cfg::kStageBytes;
-  uint64_t* my_bars = bars + warp * NS;
 
-  // ---- producer: steps of up to US units of one sequence ----------------------------------
-  int win = g0;                                  // rows of units win + lane, win + 32 + lane
-  int row_cur = unit_row(g0 + lane), row_nxt = unit_row(g0 + 32 + lane);
-  int pg = g0, ps = locate(g0);                  // next unit to ask for, its sequence
-  int p_end = min(prefix[ps + 1], g1);           // end of that sequence's units in this run
-  uint32_t present = 0;                          // US bits per stage: the unit was asked for
-  int issued = 0;
-  auto issue = [&]() {
-    const int n = min(US, p_end - pg);
-    const int stage = issued % NS;
-    const int i = lane & 15;                     // lanes 0..n-1 bring K units, 16..16+n-1 V units
-    const int at = pg + min(i, n - 1) - win;
-    const int r0 = __shfl_sync(0xffffffffu, row_cur, at & 31), r1 = __shfl_sync(0xffffffffu, row_nxt, at & 31);
-    const int row = at < 32 ? r0 : r1;
-    const uint32_t got = __ballot_sync(0xffffffffu, lane < n && row >= 0);
-    present = (present & ~(kUnitMask << (US * stage))) | (got << (US * stage));
-    uint64_t* bar = &my_bars[stage];
-    fence_proxy_async_smem();                    // the stage's reads precede its next copies
-    if (lane == 0) {
-      if (got) mbar_arrive_expect_tx(bar, 2 * Geo::kSubBytes * __popc(got));
-      else mbar_arrive(bar);                     // completes the phase with no data
+  // The next step: units [g - n, g) of sequence s, this lane's table entry.
+  int g = run.g0, s = 0, end = 0, n = 0, id = -1, half = 0;
+  auto look_up = [&]() {
+    n = 0;
+    id = -1;
+    if (g >= g1) return;
+    if (g >= end) {  // (the first time, and at a sequence's end)
+      s = end == 0 ? q4_locate(prefix, a.num_seqs, g) : s + 1;
+      end = min(prefix[s + 1], g1);
     }
-    if (lane < n && row == -2) report(a.dev_err, PA_DEVERR_BLOCK_ID);
-    __syncwarp();
-    if (i < n && row >= 0) {
-      const bool v = lane >= 16;
-      bulk_load(ring + stage * Cfg::kStageBytes + ((v ? US : 0) + i) * Geo::kSubBytes,
-                (v ? v_pool : k_pool) + static_cast<int64_t>(row) * Geo::kSubBytes, Geo::kSubBytes, bar, policy);
+    n = min(US, end - g);
+    const int fu = first_unit[s];
+    if (u < n && fu >= 0) {
+      const int un = g - prefix[s] + u, ns = sink_units(a, fu);
+      const int v = un < ns ? un : (fu & ~kSinkFlag) + un - ns;
+      id = a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + v / UPB];
+      if (id < 0) id = INT_MAX;  // no block; -1 means nothing to read
+      half = v % UPB;
     }
-    ++issued;
-    pg += n;
-    if (pg - win >= 32) {
-      win += 32;
-      row_cur = row_nxt;
-      row_nxt = unit_row(win + 32 + lane);
-    }
-    if (pg == p_end && pg < g1) {
-      ++ps;
-      p_end = min(prefix[ps + 1], g1);
+    g += n;
+  };
+  int64_t src = -1;  // byte offset of this lane's tile in the step being filled, -1: none
+  auto settle = [&]() {
+    src = -1;
+    if (id >= 0) {
+      if (id < a.num_blocks)
+        src = static_cast<int64_t>((id * a.num_kv_heads + h) * UPB + half) * Geo::kSubBytes;
+      else
+        report(a.dev_err, PA_DEVERR_BLOCK_ID);
     }
   };
-  for (int i = 0; i < NS && pg < g1; ++i) issue();
+  look_up();
+  bool active = n != 0, value = false;
+  if (active) {
+    settle();
+    look_up();
+  }
+  int slot = 0;
+  uint32_t parity = 1, polls = 0, filled = 0;  // a fresh barrier's phase of parity 1 counts as complete
+  uint64_t t0 = 0;
+  while (__any_sync(0xffffffffu, active)) {
+    const bool free_slot = active && mbar_try_wait(&empty[slot], parity);
+    const bool go = __shfl_sync(0xffffffffu, free_slot, lane & 24);
+    const uint32_t got = (__ballot_sync(0xffffffffu, src >= 0) >> (lane & 24)) & 0xffu;
+    if (go && u == 0) {
+      if (!value) present[slot] = got;
+      if (got) mbar_arrive_expect_tx(&full[slot], Geo::kSubBytes * __popc(got));
+      else mbar_arrive(&full[slot]);  // completes the phase with no data
+    }
+    __syncwarp();
+    if (go) {
+      if (src >= 0) {
+        fence_proxy_async_smem();
+        bulk_load(ring + slot * Cfg::kSlotBytes, (value ? v_pool : k_pool) + src, Geo::kSubBytes, &full[slot], policy);
+      }
+      ++filled;
+      if (++slot == NS) {
+        slot = 0;
+        parity ^= 1u;
+      }
+      value = !value;
+      if (!value) {  // both halves asked for: on to the next step
+        active = n != 0;
+        settle();
+        look_up();
+      }
+    }
+    if (__any_sync(0xffffffffu, go)) {
+      polls = 0;
+      t0 = 0;
+    } else if ((++polls & 1023u) == 0u) {  // consumers that do not come: give up after the limit
+      const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);  // one answer for the warp
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > kWaitLimitNs || polls >= kWaitMaxPolls) {
+        if (lane == 0) report(a.dev_err, PA_DEVERR_TIMEOUT);
+        break;
+      }
+    }
+  }
+  // No copy is in flight when the last warp leaves.
+  for (uint32_t i = 0; i < NS && i < filled; ++i) {
+    if (slot-- == 0) {
+      slot = NS - 1;
+      parity ^= 1u;
+    }
+    mbar_wait_bounded(&full[slot], parity ^ 1u, a.dev_err);
+  }
+}
 
-  // ---- consumer ------------------------------------------------------------------------------
+template <class Cfg>
+__device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, const UnitLists& lists, const int* prefix,
+                                           const int* first_unit, const uint8_t* ring, uint64_t* full, uint64_t* empty,
+                                           const uint32_t* present) {
+  using Geo = typename Cfg::Geo;
+  constexpr int US = Cfg::US, NS = Cfg::NS, D = Cfg::D;
+  constexpr uint32_t kUnitMask = (1u << US) - 1u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Q4Run run = q4_run<Cfg>(a, lists, q_tiles, warp);
+  const int g0 = run.g0, g1 = run.g1, h = run.h, C = run.C;
+  if (g0 >= g1) return;
+  const uint32_t my_ring = smem_addr(ring) + warp * NS * Cfg::kSlotBytes;
+  full += warp * NS;
+  empty += warp * NS;
+  present += warp * NS;
+
   Q4Warp<Cfg> st;
+  st.places(lane);
   const int g = lane >> 2, t = lane & 3;
-  const int heads = min(8, a.group - 8 * qt);    // of this run
-  const int head0 = h * a.group + 8 * qt;
-  int s = locate(g0);
+  const int heads = min(8, a.group - 8 * run.qt);
+  const int head0 = h * a.group + 8 * run.qt;
+  int s = q4_locate(prefix, a.num_seqs, g0);
   int seg0 = prefix[s], seg1 = prefix[s + 1];    // the sequence's units in the list
   int ctx = 0, ftok = 0, ub = 0, ns = 0;
+  int full0 = 0, full1 = 0;                      // units of the list whose 16 tokens are all visible
   auto begin_segment = [&]() {
-    ctx = clamp_ctx(a.context_lens[s], max_tokens);
+    ctx = clamp_ctx(a.context_lens[s], a.max_blocks_per_seq * Cfg::BS);
     ftok = first_token(a, ctx);
     ub = first_unit[s];
     ns = ub < 0 ? 0 : sink_units(a, ub);
     if (ub >= 0) ub &= ~kSinkFlag;
     if (!sinks_apart(a, ftok)) ftok = 0;
+    full0 = seg0 + ns + (ftok + 15) / 16 - ub;
+    full1 = ub < 0 ? 0 : seg0 + ns + ctx / 16 - ub;
     const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) +
                                (static_cast<int64_t>(s) * a.num_q_heads + head0 + g) * D;
     if (seg1 < g1 && t == 0 && g < heads) {      // the next sequence's query rows: into L2 now
@@ -468,7 +659,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       for (int b = 0; b < D * 2; b += 128) prefetch_l2(nq + b);
     }
     st.begin(row, g < heads, a.scale_log2, lane);
-    if (seg0 >= g0 && qt == 0 && lane == 0)      // the first piece's warp records how many there are
+    if (seg0 >= g0 && run.qt == 0 && lane == 0)  // the first piece's warp records how many there are
       a.seg_pieces[static_cast<int64_t>(s) * a.num_kv_heads + h] = (seg1 - 1) / C - seg0 / C + 1;
   };
   auto end_segment = [&]() {
@@ -480,13 +671,26 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       if (2 * t + e >= heads) continue;
       const int64_t row = row0 + 2 * t + e;
       if (whole) st.store_final(static_cast<__nv_bfloat16*>(a.out) + row * D, e, g);
-      else st.store_partial(a, row * a.max_partitions + gi - seg0 / C, e, g);
+      else st.store_partial(a, row * a.max_partitions + run.gi - seg0 / C, e, g);
     }
   };
 
+  int cg = g0, slot = 0;
+  uint32_t parity = 0;
+  // Waits for the ring's next slot; false after a timeout.
+  auto take = [&]() {
+    const bool okw = mbar_wait_bounded(&full[slot], parity, a.dev_err);
+    return __all_sync(0xffffffffu, okw) != 0;
+  };
+  auto give = [&]() {  // the slot's reads are done: it may be filled again
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[slot]);
+    if (++slot == NS) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  };
   begin_segment();
-  int done = 0, cg = g0;
-  bool timed_out = false;
   while (cg < g1) {
     if (cg == seg1) {
       end_segment();
@@ -496,40 +700,67 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       begin_segment();
     }
     const int n = min(US, min(seg1, g1) - cg);
-    const int stage = done % NS;
-    const bool okw = mbar_wait_bounded(&my_bars[stage], (done / NS) & 1, a.dev_err);
-    if (!__all_sync(0xffffffffu, okw)) {
-      timed_out = true;
-      break;
-    }
-    const uint32_t got = (present >> (US * stage)) & kUnitMask;
-    const uint8_t* data = ring + stage * Cfg::kStageBytes;
-    const int un = cg - seg0;                    // index in the sequence's units
-    const int u0 = (ub + un - ns) * 16;          // first token, past the sinks
-    int lo[US], hi[US];
-    if (got == kUnitMask && un >= ns && u0 >= ftok && u0 + 16 * US <= ctx) {
-      st.template step<false>(data, got, lo, hi, lane);
-    } else {
-      uint32_t use = 0;
-#pragma unroll
-      for (int u = 0; u < US; ++u) {
+    if (!take()) return;
+    const uint32_t got = present[slot];
+    const uint32_t kt = my_ring + slot * Cfg::kSlotBytes;
+    if (got == kUnitMask && cg >= full0 && cg + US <= full1) {
+      const bool all[2] = {false, false};
+      float x[US][4];
+      st.template logits<US, false>(kt, x, all);
+      give();
+      if (!take()) return;
+      st.template attend<US, false>(my_ring + slot * Cfg::kSlotBytes, x, all);
+      give();
+    } else {                                     // unit by unit; K's slot is held until V is done with
+      const int vslot = slot + 1 == NS ? 0 : slot + 1;
+      const bool okw = mbar_wait_bounded(&full[vslot], vslot == 0 ? parity ^ 1u : parity, a.dev_err);
+      if (!__all_sync(0xffffffffu, okw)) return;
+      const uint32_t vt = my_ring + vslot * Cfg::kSlotBytes;
+      const int un = cg - seg0;                  // index in the sequence's units
+#pragma unroll 1
+      for (int u = 0; u < n; ++u) {
+        if (!(got >> u & 1)) continue;
         const bool sink = un + u < ns;
-        lo[u] = sink ? 0 : ftok - (u0 + 16 * u);
-        hi[u] = min(16, sink ? a.num_sinks - 16 * (un + u) : ctx - (u0 + 16 * u));
-        if ((got >> u & 1) && lo[u] < hi[u] && lo[u] < 16 && hi[u] > 0) use |= 1u << u;
+        const int u0 = (sink ? un + u : ub + un + u - ns) * 16;  // first token
+        const int lo = sink ? 0 : ftok - u0, hi = (sink ? a.num_sinks : ctx) - u0;
+        const bool out[2] = {st.tok < lo || st.tok >= hi, st.tok + 8 < lo || st.tok + 8 >= hi};
+        float x[1][4];
+        st.template logits<1, true>(kt + u * Geo::kSubBytes, x, out);
+        st.template attend<1, true>(vt + u * Geo::kSubBytes, x, out);
       }
-      if (use) st.template step<true>(data, use, lo, hi, lane);
+      give();
+      give();
     }
-    __syncwarp();
     cg += n;
-    ++done;
-    if (pg < g1) issue();
   }
-  if (timed_out) {
-    // Give copies still in flight a bounded chance to land before leaving.
-    for (int j = done; j < issued; ++j) mbar_wait_bounded(&my_bars[j % NS], (j / NS) & 1, a.dev_err);
+  end_segment();
+}
+
+// q_tiles: runs of 8 query heads per KV head, ceil(group / 8).
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::kThreads, 1)
+    paged_decode_q4_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool, int q_tiles,
+                           const SinksArgs a) {
+  constexpr int W = Cfg::W, NS = Cfg::NS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + Cfg::kRingBytes);
+  uint64_t* empty = full + W * NS;
+  uint32_t* present = reinterpret_cast<uint32_t*>(empty + W * NS);
+  int* prefix = reinterpret_cast<int*>(present + W * NS);  // [B + 1] units before sequence s
+  int* first_unit = prefix + a.num_seqs + 1;               // [B]
+
+  grid_dependents_launch();  // the merge grid may be scheduled; it waits for this grid before it reads
+  if (threadIdx.x < 2 * W * NS) mbar_init(&full[threadIdx.x], 1);
+  fence_barrier_init();
+  const UnitLists lists = build_unit_lists<W + 4>(a, Cfg::BS, prefix, first_unit);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
+  if (warp < W) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kConsumerRegs));
+    q4_consume<Cfg>(a, q_tiles, lists, prefix, first_unit, ring, full, empty, present);
   } else {
-    end_segment();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kProducerRegs));
+    q4_produce<Cfg>(k_pool, v_pool, a, q_tiles, lists, prefix, first_unit, ring, full, empty, present, warp - W);
   }
 }
 
