@@ -205,9 +205,11 @@ def _ptr(t) -> int:
 
 
 def _stream_ptr(stream) -> int:
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: torch.cuda.current_stream() builds a Stream object,
+        # 3.2 us a call against 0.2
+        torch = _torch()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -467,25 +469,23 @@ def _bad(msg):
     return InvalidArgumentError(PA_ERR_INVALID_ARG, msg)
 
 
-def _on_device(device, *tensors):
-    """Contiguous tensors on `device`, which is the current one."""
-    torch = _torch()
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise _bad("tensors must be on the current CUDA device")
+def _on_device(*tensors):
+    """Contiguous tensors on the current CUDA device."""
+    dev = _torch()._C._cuda_getDevice() if tensors[0].is_cuda else None
     for t in tensors:
-        if t is not None and (t.device != device or not t.is_contiguous()):
-            raise _bad("tensors must be contiguous and on one CUDA device")
+        if t.get_device() != dev or not t.is_contiguous():
+            raise _bad("tensors must be contiguous and on the current CUDA device")
 
 
 def _token_rows(t, heads, head_dim, what):
     """Elements between the tokens of a [tokens, heads, head_dim] tensor whose
     heads and dims are contiguous (a slice of a fused product, or whole)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
-        raise _bad(f"{what} must be [tokens, {heads}, {head_dim}]")
+    if t.is_contiguous():
+        return heads * head_dim
     st, sh, sd = t.stride()
-    if (sd != 1 and head_dim != 1) or (sh != head_dim and heads > 1):
+    if sd != 1 or (sh != head_dim and heads > 1):
         raise _bad(f"{what}: heads and dims must be contiguous")
-    return st if t.shape[0] > 1 else heads * head_dim
+    return st if t.size(0) > 1 else heads * head_dim
 
 
 def decode_split_sinks(q, k_pool, v_pool, block_tables, context_lens, scale: float, window: int,
@@ -542,13 +542,14 @@ def kv_append_q4(k_new, v_new, slot_mapping, k_pool, v_pool, dev_err=None, strea
     """pa_kv_append_q4: quantises new rows (bf16, heads and dims contiguous)
     into their slots of 4-bit pools."""
     torch = _torch()
-    T, Hkv, D = k_new.shape
+    shape = T, Hkv, D = k_new.shape
     NB, H2, BS = _q4_pool_shape(k_pool, v_pool, D)
-    _on_device(k_pool.device, k_pool, v_pool, slot_mapping)
+    _on_device(k_pool, v_pool, slot_mapping)
+    dev = k_pool.get_device()
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or H2 != Hkv:
         raise _bad("slot_mapping must be int64 [tokens] and the pools' heads those of k_new")
-    if (v_new.shape != k_new.shape or k_new.dtype != v_new.dtype or k_new.device != k_pool.device
-            or v_new.device != k_pool.device):
+    if (v_new.shape != shape or k_new.dtype != v_new.dtype or k_new.get_device() != dev
+            or v_new.get_device() != dev):
         raise _bad("k_new and v_new must match in shape, type and device")
     _check(library().pa_kv_append_q4(
         k_new.data_ptr(), v_new.data_ptr(), _token_rows(k_new, Hkv, D, "k_new"),
@@ -561,19 +562,19 @@ def kv_gather_q4(k_pool, v_pool, slot_mapping, head_dim: int, dtype=None, out=No
                  stream=None):
     """pa_kv_gather_q4: the values of 4-bit rows, (k, v) of [tokens, heads,
     head_dim] in ``dtype`` (bf16 unless given). Rows of negative slots keep what
-    ``out`` held (zeros if it is made here)."""
+    ``out`` held; without ``out`` they are uninitialised."""
     torch = _torch()
     NB, Hkv, BS = _q4_pool_shape(k_pool, v_pool, head_dim)
-    _on_device(k_pool.device, k_pool, v_pool, slot_mapping)
+    _on_device(k_pool, v_pool, slot_mapping)
     if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1:
         raise _bad("slot_mapping must be int64 [tokens]")
-    T = slot_mapping.shape[0]
+    T = slot_mapping.size(0)
     if out is None:
-        both = torch.zeros((2, T, Hkv, head_dim), dtype=dtype or torch.bfloat16, device=k_pool.device)
-        k_out, v_out = both[0], both[1]
+        k_out = torch.empty((T, Hkv, head_dim), dtype=dtype or torch.bfloat16, device=k_pool.device)
+        v_out = torch.empty_like(k_out)
     else:
         k_out, v_out = out
-        _on_device(k_pool.device, k_out, v_out)
+        _on_device(k_pool, k_out, v_out)
         if (k_out.shape != (T, Hkv, head_dim) or v_out.shape != k_out.shape
                 or v_out.dtype != k_out.dtype or (dtype is not None and dtype != k_out.dtype)):
             raise _bad("out must be two [tokens, heads, head_dim] tensors of one type")
@@ -592,15 +593,15 @@ def decode_q4(q, k_pool, v_pool, block_tables, context_lens, scale: float, windo
     torch = _torch()
     if out is None:
         out = torch.empty_like(q)
-    B, Hq, D = q.shape
+    shape = B, Hq, D = q.shape
     NB, Hkv, BS = _q4_pool_shape(k_pool, v_pool, D)
-    _on_device(q.device, q, k_pool, v_pool, block_tables, context_lens, out)
-    if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32
-            or block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,)):
+    _on_device(q, k_pool, v_pool, block_tables, context_lens, out)
+    rows, MBS = block_tables.shape
+    if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or rows != B
+            or context_lens.shape != (B,)):
         raise _bad("block_tables must be int32 [seqs, blocks], context_lens int32 [seqs]")
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.shape != shape or out.dtype != q.dtype:
         raise _bad("out must match q")
-    MBS = block_tables.shape[1]
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
     _check(library().pa_decode_q4(
@@ -634,44 +635,45 @@ def rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_pool, v_po
     and k by their positions and writes k and v into their slots. q may be
     None; returns the rotated queries (None without q)."""
     torch = _torch()
-    T, Hkv, D = k_new.shape
-    dev = k_pool.device
+    shape = T, Hkv, D = k_new.shape
+    dtype = k_new.dtype
     q4 = k_pool.dtype == torch.uint8
     if q4:
         NB, H2, BS = _q4_pool_shape(k_pool, v_pool, D)
     else:
-        if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.shape[3] != D:
+        NB, H2, BS, D2 = k_pool.shape
+        if D2 != D or v_pool.shape != k_pool.shape:
             raise _bad("pools must be [num_blocks, num_kv_heads, block_size, head_dim]")
-        if k_pool.dtype != k_new.dtype or v_pool.dtype != k_new.dtype:
+        if k_pool.dtype != dtype or v_pool.dtype != dtype:
             raise _bad("pools must have the type of k_new")
-        NB, H2, BS, _ = k_pool.shape
-    _on_device(dev, k_pool, v_pool, slot_mapping, positions, inv_freq)
+    _on_device(k_pool, v_pool, slot_mapping, positions, inv_freq)
+    dev = k_pool.get_device()
     if (positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64
             or inv_freq.dtype != torch.float32 or positions.shape != (T,)
             or slot_mapping.shape != (T,) or inv_freq.dim() != 1 or H2 != Hkv):
         raise _bad("positions int32 [tokens], slot_mapping int64 [tokens], inv_freq fp32")
-    if (v_new.shape != k_new.shape or v_new.dtype != k_new.dtype or k_new.device != dev
-            or v_new.device != dev):
+    if (v_new.shape != shape or v_new.dtype != dtype or k_new.get_device() != dev
+            or v_new.get_device() != dev):
         raise _bad("k_new and v_new must match in shape, type and device")
-    Hq = q_stride = 0
+    Hq = q_stride = q_ptr = out_ptr = 0
     if q is not None:
-        Hq = q.shape[1]
-        if q.shape[0] != T or q.dtype != k_new.dtype or q.device != dev:
-            raise _bad("q must have the tokens, type and device of k_new")
+        rows, Hq, Dq = q.shape
+        if rows != T or Dq != D or q.dtype != dtype or q.get_device() != dev:
+            raise _bad("q must have the tokens, head_dim, type and device of k_new")
         q_stride = _token_rows(q, Hq, D, "q")
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-        elif (q_out.shape != (T, Hq, D) or q_out.dtype != q.dtype or q_out.device != dev
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        elif (q_out.shape != q.shape or q_out.dtype != dtype or q_out.get_device() != dev
               or not q_out.is_contiguous()):
             raise _bad("q_out must be contiguous, of q's shape and type")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     fn = library().pa_rope_append_q4 if q4 else library().pa_rope_append
-    _check(fn(_ptr(q), k_new.data_ptr(), v_new.data_ptr(), q_stride,
+    _check(fn(q_ptr, k_new.data_ptr(), v_new.data_ptr(), q_stride,
               _token_rows(k_new, Hkv, D, "k_new"), _token_rows(v_new, Hkv, D, "v_new"),
               positions.data_ptr(), inv_freq.data_ptr(), slot_mapping.data_ptr(), T, Hq, Hkv, D,
-              2 * inv_freq.shape[0], 1 if interleaved else 0, mscale, BS, NB, _dtype_code(k_new),
-              _ptr(q_out), k_pool.data_ptr(), v_pool.data_ptr(), _ptr(dev_err),
-              _stream_ptr(stream)))
-    return q_out
+              2 * inv_freq.size(0), 1 if interleaved else 0, mscale, BS, NB, _dtype_code(k_new),
+              out_ptr, k_pool.data_ptr(), v_pool.data_ptr(), _ptr(dev_err), _stream_ptr(stream)))
+    return q_out if q is not None else None
 
 
 @dataclass
@@ -701,26 +703,27 @@ def extend_tables(block_tables, context_lens, new_lens, free_queue, queue_state,
     returns its StepTables. ``out`` shares nothing with the inputs: a loop keeps
     two and swaps them."""
     torch = _torch()
-    dev = block_tables.device
     B, MBS = block_tables.shape
     if out is None:
-        out = StepTables.empty(B, max_tokens, dev)
-    _on_device(dev, block_tables, context_lens, new_lens, free_queue, queue_state, out.context_lens,
-               out.query_start, out.positions, out.slot_mapping, out.queue_state)
+        out = StepTables.empty(B, max_tokens, block_tables.device)
+    lens, start, pos, slots, state = (out.context_lens, out.query_start, out.positions,
+                                      out.slot_mapping, out.queue_state)
+    _on_device(block_tables, context_lens, new_lens, free_queue, queue_state, lens, start, pos,
+               slots, state)
     i32 = torch.int32
-    for t, n in ((block_tables, B * MBS), (context_lens, B), (new_lens, B),
-                 (free_queue, free_queue.numel()), (queue_state, 2), (out.context_lens, B),
-                 (out.query_start, B + 1), (out.positions, max_tokens), (out.queue_state, 2)):
-        if t.dtype != i32 or t.numel() != n:
-            raise _bad("tables, lengths, queue and outputs must be int32 of the batch's sizes")
-    if out.slot_mapping.dtype != torch.int64 or out.slot_mapping.numel() != max_tokens:
-        raise _bad("slot_mapping must be int64 [max_tokens]")
+    if not (block_tables.dtype == context_lens.dtype == new_lens.dtype == free_queue.dtype
+            == queue_state.dtype == lens.dtype == start.dtype == pos.dtype == state.dtype == i32):
+        raise _bad("tables, lengths, queue, states and positions must be int32")
+    if (context_lens.numel() != B or new_lens.numel() != B or lens.numel() != B
+            or start.numel() != B + 1 or queue_state.numel() != 2 or state.numel() != 2
+            or pos.numel() != max_tokens or slots.numel() != max_tokens
+            or slots.dtype != torch.int64):
+        raise _bad("lengths, states and outputs must have the batch's sizes, slot_mapping int64")
     _check(library().pa_extend_tables(
         block_tables.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(), B, MBS,
         int(block_size), free_queue.data_ptr(), free_queue.numel(), queue_state.data_ptr(),
-        int(max_tokens), out.context_lens.data_ptr(), out.query_start.data_ptr(),
-        out.positions.data_ptr(), out.slot_mapping.data_ptr(), out.queue_state.data_ptr(),
-        _ptr(dev_err), _stream_ptr(stream)))
+        int(max_tokens), lens.data_ptr(), start.data_ptr(), pos.data_ptr(), slots.data_ptr(),
+        state.data_ptr(), _ptr(dev_err), _stream_ptr(stream)))
     return out
 
 

@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -195,27 +196,42 @@ __device__ __forceinline__ uint32_t codes8(const Vec16& x, const Quant& g) {
 // Writes an item (vectors c0 and c1 of 8 dims) of token `slot`, KV head h, to
 // a 4-bit pool; called by all lanes of the head's threads together (lanes
 // whose token is not written pass slot < 0 and only take part in the
-// shuffles). Each 64-dim group's spread is folded over the head's D / 16
-// lanes; a lane adds what its vectors hold of the group.
-template <int D, bool kValue>
+// shuffles). kSplit: c0 and c1 may lie in different 64-dim groups (a rotated
+// half layout), and each group's spread is folded over all of the head's D / 16
+// lanes, a lane adding what its vectors hold of the group; otherwise an item
+// is 16 neighbouring dims and four neighbouring lanes hold a group.
+template <int D, bool kValue, bool kSplit>
 __device__ __forceinline__ void store_q4(uint8_t* pool, const Vec16& a, const Vec16& b, int c0, int c1,
                                          int item, int64_t slot, int h, const RopeArgs& p) {
   using Geo = Q4Geo<D>;
   constexpr uint32_t kNone = 0x7f807f80u;  // (+inf, +inf): neutral for min
   const uint32_t sa = spread8(a), sb = spread8(b);
-  Quant ga{}, gb{};
-  uint32_t mine = 0;
+  Quant ga, gb;
+  uint32_t mine = 0;  // the parameters that this lane writes, of group `item` or item / 4
+  if constexpr (kSplit) {
+    uint32_t spread_a = 0, spread_b = 0, spread_i = 0;
 #pragma unroll
-  for (int g = 0; g < Geo::kGroups; ++g) {
-    uint32_t s = kNone;
-    if (c0 >> 3 == g) s = sa;
-    if (c1 >> 3 == g) s = min_bf16x2(s, sb);
+    for (int g = 0; g < Geo::kGroups; ++g) {
+      uint32_t s = kNone;
+      if (c0 >> 3 == g) s = sa;
+      if (c1 >> 3 == g) s = min_bf16x2(s, sb);
 #pragma unroll
-    for (int off = D / 32; off >= 1; off >>= 1) s = min_bf16x2(s, __shfl_xor_sync(0xffffffffu, s, off));
-    const Quant q = group_params(s);
-    if (c0 >> 3 == g) ga = q;
-    if (c1 >> 3 == g) gb = q;
-    if (item == g) mine = q.param;
+      for (int off = D / 32; off >= 1; off >>= 1) s = min_bf16x2(s, __shfl_xor_sync(0xffffffffu, s, off));
+      if (c0 >> 3 == g) spread_a = s;
+      if (c1 >> 3 == g) spread_b = s;
+      if (item == g) spread_i = s;
+    }
+    ga = group_params(spread_a);
+    gb = group_params(spread_b);
+    // the lane that writes group `item`'s parameters may hold neither of its vectors
+    if (item < Geo::kGroups)
+      mine = spread_i == spread_a ? ga.param : spread_i == spread_b ? gb.param : group_params(spread_i).param;
+  } else {
+    uint32_t s = min_bf16x2(sa, sb);
+    s = min_bf16x2(s, __shfl_xor_sync(0xffffffffu, s, 1));
+    s = min_bf16x2(s, __shfl_xor_sync(0xffffffffu, s, 2));
+    ga = gb = group_params(s);
+    mine = ga.param;
   }
   if (slot < 0) return;
   const int64_t blk = slot >> p.block_shift;
@@ -225,15 +241,18 @@ __device__ __forceinline__ void store_q4(uint8_t* pool, const Vec16& a, const Ve
   uint8_t* row = sub + tok * Geo::kRowBytes;
   *reinterpret_cast<uint32_t*>(row + Geo::template word<kValue>(tok, c0)) = codes8(a, ga);
   *reinterpret_cast<uint32_t*>(row + Geo::template word<kValue>(tok, c1)) = codes8(b, gb);
-  if (item < Geo::kGroups)
-    *reinterpret_cast<uint32_t*>(sub + Geo::kCodeBytes + tok * Geo::kParamRow + item * 4) = mine;
+  const int group = kSplit ? item : (item & 3) == 0 ? item >> 2 : Geo::kGroups;
+  if (group < Geo::kGroups)
+    *reinterpret_cast<uint32_t*>(sub + Geo::kCodeBytes + tok * Geo::kParamRow + group * 4) = mine;
 }
 
 // grid.x walks tiles of tile_tokens tokens, grid.y slices of a tile's items.
-template <typename T, int D, bool kInterleaved, bool kQ4>
+// kRotate: rotary_dim may be above 0.
+template <typename T, int D, bool kInterleaved, bool kQ4, bool kRotate>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs p) {
   constexpr int N = VecOf<T>::N;
   constexpr int kItems = D / (2 * N);  // items (threads) of one head
+  constexpr bool kSplit = kRotate && !kInterleaved;
   extern __shared__ float2 cs[];       // [tile_tokens][rotary_dim / 2]
   const int tid = threadIdx.x;
   const int half = p.rotary_dim / 2;
@@ -243,7 +262,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
   for (int tile = blockIdx.x; tile * static_cast<int64_t>(p.tile_tokens) < p.num_tokens; tile += gridDim.x) {
     const int64_t tok0 = tile * static_cast<int64_t>(p.tile_tokens);
     const int nt = static_cast<int>(min(static_cast<int64_t>(p.tile_tokens), p.num_tokens - tok0));
-    for (int i = tid; i < nt * half; i += kRopeThreads) {
+    for (int i = tid; kRotate && i < nt * half; i += kRopeThreads) {
       const int t = i / half;
       const double u = static_cast<double>(p.positions[tok0 + t]) *
                        (static_cast<double>(p.inv_freq[i - t * half]) * 0.31830988618379067154);
@@ -251,7 +270,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
       sincospif(static_cast<float>(u - 2.0 * rint(0.5 * u)), &s, &c);
       cs[i] = make_float2(c * p.mscale, s * p.mscale);
     }
-    __syncthreads();
+    if (kRotate) __syncthreads();
 
     const int total = nt * heads * kItems;
     const int step = gridDim.y * kRopeThreads;
@@ -265,7 +284,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
         const int item = i % kItems, th = i / kItems;
         tk[u] = th / heads;
         hd[u] = th - tk[u] * heads;
-        const bool rotated = item < rot_items;
+        const bool rotated = kRotate && item < rot_items && hd[u] < p.num_q_heads + p.num_kv_heads;
         c0[u] = !kInterleaved && rotated ? item : 2 * item;
         c1[u] = !kInterleaved && rotated ? item + rot_items : 2 * item + 1;
         if (i >= total) {
@@ -290,7 +309,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
         const int item = (base + u * step + tid) % kItems;
         const bool is_q = hd[u] >= 0 && hd[u] < p.num_q_heads;
         const bool is_v = hd[u] >= p.num_q_heads + p.num_kv_heads;
-        if (hd[u] >= 0 && !is_v && item < rot_items)
+        if (kRotate && hd[u] >= 0 && !is_v && item < rot_items)
           rotate<T, kInterleaved>(a[u], b[u], cs + tk[u] * half, item * N);
         const int64_t t = tok0 + tk[u];
         if (is_q) {
@@ -313,11 +332,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
           const bool any_k = __any_sync(0xffffffffu, slot >= 0 && !is_v);
           const bool any_v = __any_sync(0xffffffffu, slot >= 0 && is_v);
           if (any_k)
-            store_q4<D, false>(static_cast<uint8_t*>(p.k_pool), a[u], b[u], c0[u], c1[u], item,
-                               is_v ? -1 : slot, h, p);
+            store_q4<D, false, kSplit>(static_cast<uint8_t*>(p.k_pool), a[u], b[u], c0[u], c1[u], item,
+                                       is_v ? -1 : slot, h, p);
           if (any_v)
-            store_q4<D, true>(static_cast<uint8_t*>(p.v_pool), a[u], b[u], c0[u], c1[u], item,
-                              is_v ? slot : -1, h, p);
+            store_q4<D, true, false>(static_cast<uint8_t*>(p.v_pool), a[u], b[u], c0[u], c1[u], item,
+                                     is_v ? slot : -1, h, p);
         } else if (slot >= 0) {
           const int64_t blk = slot >> p.block_shift;
           const int64_t row = ((blk * p.num_kv_heads + h) << p.block_shift) + (slot & (p.block_size - 1));
@@ -327,54 +346,73 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
         }
       }
     }
-    __syncthreads();  // cs is rewritten for the next tile
+    if (kRotate) __syncthreads();  // cs is rewritten for the next tile
   }
 }
 
-// Values of 4-bit rows: one thread per eight dims of K and of V.
+// Values of 4-bit rows. A thread takes the same eight dims of the same head of
+// K and of V in every token that it visits, kGatherUnroll tokens at a time, so
+// that only the slots differ; grid.x walks tokens, grid.y a token's octets.
+constexpr int kGatherThreads = 256, kGatherUnroll = 2;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kGatherThreads)
     kv_gather_q4_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
                         const int64_t* __restrict__ slots, int num_tokens, int num_kv_heads, int block_shift,
                         int64_t num_slots, T* __restrict__ k_out, T* __restrict__ v_out, uint32_t* dev_err) {
   using Geo = Q4Geo<D>;
   constexpr int C = D / 8;
-  const int64_t total = static_cast<int64_t>(num_tokens) * num_kv_heads * C;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int c = static_cast<int>(i % C);
-    const int64_t th = i / C;
-    const int64_t t = th / num_kv_heads;
-    const int64_t h = th - t * num_kv_heads;
-    const int64_t slot = slots[t];
-    if (slot < 0) continue;
-    if (slot >= num_slots) {
-      if (c == 0 && h == 0) report(dev_err, PA_DEVERR_SLOT);
-      continue;
+  const int per_token = num_kv_heads * C;
+  // tokens side by side in a block, and this thread's token and octet
+  const int width = min(per_token, kGatherThreads), side = kGatherThreads / width;
+  const int mine = threadIdx.x / width;
+  const int item = blockIdx.y * width + (threadIdx.x - mine * width);
+  if (mine >= side || item >= per_token) return;
+  const int c = item % C, h = item / C;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * side;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * side + mine; t0 < num_tokens; t0 += step * kGatherUnroll) {
+    int64_t tok_at[kGatherUnroll];
+    uint32_t w[kGatherUnroll][2], q[kGatherUnroll][2];
+#pragma unroll
+    for (int u = 0; u < kGatherUnroll; ++u) {
+      const int64_t t = t0 + u * step;
+      tok_at[u] = -1;
+      if (t >= num_tokens) continue;
+      const int64_t slot = slots[t];
+      if (slot < 0) continue;
+      if (slot >= num_slots) {
+        if (item == 0) report(dev_err, PA_DEVERR_SLOT);
+        continue;
+      }
+      tok_at[u] = t;
+      const int64_t blk = slot >> block_shift;
+      const int off = static_cast<int>(slot) & ((1 << block_shift) - 1);
+      const int tok = off & 15;
+      const int64_t sub = (((blk * num_kv_heads + h) << (block_shift - 4)) + (off >> 4)) * Geo::kSubBytes;
+      const int64_t row = sub + tok * Geo::kRowBytes;
+      const int64_t par = sub + Geo::kCodeBytes + tok * Geo::kParamRow + (c >> 3) * 4;
+      w[u][0] = *reinterpret_cast<const uint32_t*>(k_pool + row + Geo::k_word(tok, c));
+      w[u][1] = *reinterpret_cast<const uint32_t*>(v_pool + row + Geo::v_word(tok, c));
+      q[u][0] = *reinterpret_cast<const uint32_t*>(k_pool + par);
+      q[u][1] = *reinterpret_cast<const uint32_t*>(v_pool + par);
     }
-    const int64_t blk = slot >> block_shift;
-    const int off = static_cast<int>(slot) & ((1 << block_shift) - 1);
-    const int tok = off & 15;
-    const int64_t sub = (((blk * num_kv_heads + h) << (block_shift - 4)) + (off >> 4)) * Geo::kSubBytes;
-    const int64_t row = sub + tok * Geo::kRowBytes;
-    const int64_t par = sub + Geo::kCodeBytes + tok * Geo::kParamRow + (c >> 3) * 4;
-    const uint32_t w[2] = {*reinterpret_cast<const uint32_t*>(k_pool + row + Geo::k_word(tok, c)),
-                           *reinterpret_cast<const uint32_t*>(v_pool + row + Geo::v_word(tok, c))};
-    const uint32_t q[2] = {*reinterpret_cast<const uint32_t*>(k_pool + par),
-                           *reinterpret_cast<const uint32_t*>(v_pool + par)};
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      T* out = (kv ? v_out : k_out) + th * D + c * 8;
-      float f[8];
+    for (int u = 0; u < kGatherUnroll; ++u) {
+      if (tok_at[u] < 0) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)  // 2^23 + code, exactly
-        f[j] = fmaf(__uint_as_float(0x4b000000u | ((w[kv] >> (4 * j)) & 15u)) - 8388608.f, bf16_lo(q[kv]),
-                    bf16_hi(q[kv]));
-      if constexpr (sizeof(T) == 2) {
-        store16(out, VecOf<T>::narrow(f));
-      } else {
-        reinterpret_cast<float4*>(out)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(out)[1] = make_float4(f[4], f[5], f[6], f[7]);
+      for (int kv = 0; kv < 2; ++kv) {
+        T* out = (kv ? v_out : k_out) + (tok_at[u] * num_kv_heads + h) * D + c * 8;
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)  // 2^23 + code, exactly
+          f[j] = fmaf(__uint_as_float(0x4b000000u | ((w[u][kv] >> (4 * j)) & 15u)) - 8388608.f, bf16_lo(q[u][kv]),
+                      bf16_hi(q[u][kv]));
+        if constexpr (sizeof(T) == 2) {
+          store16(out, VecOf<T>::narrow(f));
+        } else {
+          reinterpret_cast<float4*>(out)[0] = make_float4(f[0], f[1], f[2], f[3]);
+          reinterpret_cast<float4*>(out)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
       }
     }
   }
@@ -382,14 +420,22 @@ __global__ void __launch_bounds__(256)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Multiprocessors of the current device, asked for once per device.
 int sm_count() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 148;
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 148;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (n <= 0) n = 148;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
-template <typename T, int D, bool kInterleaved, bool kQ4>
+template <typename T, int D, bool kInterleaved, bool kQ4, bool kRotate>
 void launch_rope(RopeArgs p, cudaStream_t stream) {
   const int sms = sm_count();
   const int heads = p.num_q_heads + 2 * p.num_kv_heads;
@@ -402,16 +448,19 @@ void launch_rope(RopeArgs p, cudaStream_t stream) {
   const int64_t rounds = (items + kRopeThreads * kUnroll - 1) / (kRopeThreads * kUnroll);
   int gy = 1;
   while (gy < rounds && tiles * gy < 4 * sms) ++gy;
-  const int64_t gx = std::min<int64_t>(tiles, static_cast<int64_t>(sms) * 8);
+  // One tile a CTA: a grid of 8 CTAs per SM walking the tiles leaves some with 4
+  // tiles and others with 3 at 16384 tokens.
+  const int64_t gx = std::min<int64_t>(tiles, 1 << 30);
   const size_t smem = static_cast<size_t>(p.tile_tokens) * (p.rotary_dim / 2) * sizeof(float2);
-  rope_append_kernel<T, D, kInterleaved, kQ4>
+  rope_append_kernel<T, D, kInterleaved, kQ4, kRotate>
       <<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kRopeThreads, smem, stream>>>(p);
 }
 
 template <typename T, int D, bool kQ4>
 void pick_layout(const RopeArgs& p, bool interleaved, cudaStream_t stream) {
-  if (interleaved) launch_rope<T, D, true, kQ4>(p, stream);
-  else launch_rope<T, D, false, kQ4>(p, stream);
+  if (p.rotary_dim == 0) launch_rope<T, D, false, kQ4, false>(p, stream);
+  else if (interleaved) launch_rope<T, D, true, kQ4, true>(p, stream);
+  else launch_rope<T, D, false, kQ4, true>(p, stream);
 }
 
 template <typename T, bool kQ4>
@@ -486,9 +535,11 @@ pa_status_t run_rope(RopeArgs p, int head_dim, bool interleaved, int num_blocks,
 template <typename T, int D>
 void launch_gather(const void* k_pool, const void* v_pool, const int64_t* slots, int T_, int H, int bs,
                    int64_t num_slots, void* k_out, void* v_out, uint32_t* err, cudaStream_t st) {
-  const int64_t total = static_cast<int64_t>(T_) * H * (D / 8);
-  const int grid = static_cast<int>(std::min<int64_t>((total + 255) / 256, static_cast<int64_t>(sm_count()) * 16));
-  kv_gather_q4_kernel<T, D><<<grid, 256, 0, st>>>(
+  const int per_token = H * (D / 8), width = std::min(per_token, kGatherThreads), side = kGatherThreads / width;
+  const int gy = (per_token + width - 1) / width;
+  const int64_t gx = std::min<int64_t>((static_cast<int64_t>(T_) + side * kGatherUnroll - 1) / (side * kGatherUnroll), 1 << 30);
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  kv_gather_q4_kernel<T, D><<<grid, kGatherThreads, 0, st>>>(
       static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), slots, T_, H, bs == 16 ? 4 : 5, num_slots,
       static_cast<T*>(k_out), static_cast<T*>(v_out), err);
 }
@@ -588,6 +639,8 @@ pa_status_t pa_kv_gather_q4(const void* k_pool, const void* v_pool, const int64_
   if (dtype != PA_F32 && dtype != PA_BF16) return fail(PA_ERR_INVALID_ARG, "unknown dtype");
   if (pa_q4_tile_bytes(block_size, head_dim) == 0)
     return fail(PA_ERR_UNSUPPORTED, "no 4-bit cache for head_dim=%d block_size=%d", head_dim, block_size);
+  if (static_cast<int64_t>(num_kv_heads) * head_dim >= (int64_t(1) << 24))  // (grid.y)
+    return fail(PA_ERR_UNSUPPORTED, "too many heads");
   if (num_tokens == 0) return ok();
   if (k_pool == nullptr || v_pool == nullptr || slot_mapping == nullptr || k_out == nullptr || v_out == nullptr)
     return fail(PA_ERR_INVALID_ARG, "NULL pointer");

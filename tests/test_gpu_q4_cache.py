@@ -102,7 +102,8 @@ def test_bad_slots_and_repeated_reads():
     assert torch.all(kp[1:] == 0xA5)
     err.zero_()
     again = torch.tensor([0, 0, 1, 1 << 50, 0, -1], device="cuda")
-    a, _ = binding.kv_gather_q4(kp, vp, again, D, dev_err=err)
+    out = torch.zeros(2, 6, H, D, dtype=torch.bfloat16, device="cuda")
+    a, _ = binding.kv_gather_q4(kp, vp, again, D, out=(out[0], out[1]), dev_err=err)
     assert int(err.item()) == binding.DEVERR_SLOT
     assert torch.equal(a[0], a[1]) and torch.equal(a[0], a[4]) and torch.all(a[3] == 0) and torch.all(a[5] == 0)
 
