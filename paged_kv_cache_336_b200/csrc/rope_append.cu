@@ -157,7 +157,11 @@ struct Quant {
 __device__ __forceinline__ Quant group_params(uint32_t spread) {
   const float mn = bf16_lo(spread), mx = -bf16_hi(spread);
   Quant g;
-  float s = __fdiv_rn(0.5f * mx - 0.5f * mn, 7.5f);
+  const float half = 0.5f * mx - 0.5f * mn;
+  // the correctly rounded quotient again; residuals of small ranges may underflow
+  constexpr float kInv = 1.f / 7.5f;
+  const float q0 = half * kInv;
+  float s = half >= 0x1p-100f ? fmaf(fmaf(-q0, 7.5f, half), kInv, q0) : __fdiv_rn(half, 7.5f);
   float m = mn;
   if (!(fabsf(mn) < INFINITY) || !(fabsf(mx) < INFINITY)) s = m = __uint_as_float(0x7fc00000u);
   const uint32_t packed = pack_bf16x2(s, m);
@@ -169,19 +173,22 @@ __device__ __forceinline__ Quant group_params(uint32_t spread) {
   return g;
 }
 
-// Codes of eight elements, dim 0 in the lowest nibble.
+// Codes of eight elements, dim 0 in the lowest nibble. Adding 1.5 * 2^23 leaves
+// rint(q) in the low mantissa bits; shifted sums of those words hold the codes
+// and a constant.
 __device__ __forceinline__ uint32_t codes8(const Vec16& x, const Quant& g) {
   float f[8];
   VecOf<__nv_bfloat16>::widen(x, f);
   uint32_t word = 0;
   if (g.r > 0.f) {
+    constexpr uint32_t kBias = 0x4b400000u * 0x11111111u;  // mod 2^32
+    word = 0u - kBias;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float d = f[i] - g.mn;
       float q = d * g.r;
-      q = fmaf(fmaf(-q, g.s, d), g.r, q);  // the correctly rounded d / s
-      q = fminf(q, 15.f) + 12582912.f;     // rint in the low mantissa bits (q >= 0)
-      word |= (__float_as_uint(q) & 15u) << (4 * i);
+      q = fmaf(fmaf(-q, g.s, d), g.r, q);  // the correctly rounded d / s, at most 15 (1 + 2^-8): no clamp
+      word += __float_as_uint(q + 12582912.f) << (4 * i);
     }
   } else if (g.s > 0.f) {  // a scale near the ends of the range: halves, and a division
 #pragma unroll
@@ -192,6 +199,22 @@ __device__ __forceinline__ uint32_t codes8(const Vec16& x, const Quant& g) {
   }  // s == 0 (all equal, or a spread below half the smallest scale) or NaN: codes 0
   return word;
 }
+
+// Where a slot's code row and its parameters stand in a pool.
+template <int D>
+struct Q4Place {
+  int64_t row, params;
+  int tok;
+  __device__ __forceinline__ Q4Place(int64_t slot, int64_t h, int num_kv_heads, int block_shift) {
+    using Geo = Q4Geo<D>;
+    const int64_t blk = slot >> block_shift;
+    const int off = static_cast<int>(slot) & ((1 << block_shift) - 1);
+    tok = off & 15;
+    const int64_t sub = (((blk * num_kv_heads + h) << (block_shift - 4)) + (off >> 4)) * Geo::kSubBytes;
+    row = sub + tok * Geo::kRowBytes;
+    params = sub + Geo::kCodeBytes + tok * Geo::kParamRow;
+  }
+};
 
 // Writes an item (vectors c0 and c1 of 8 dims) of token `slot`, KV head h, to
 // a 4-bit pool; called by all lanes of the head's threads together (lanes
@@ -234,25 +257,19 @@ __device__ __forceinline__ void store_q4(uint8_t* pool, const Vec16& a, const Ve
     mine = ga.param;
   }
   if (slot < 0) return;
-  const int64_t blk = slot >> p.block_shift;
-  const int off = static_cast<int>(slot) & (p.block_size - 1);
-  const int tok = off & 15;
-  uint8_t* sub = pool + (((blk * p.num_kv_heads + h) << (p.block_shift - 4)) + (off >> 4)) * Geo::kSubBytes;
-  uint8_t* row = sub + tok * Geo::kRowBytes;
-  *reinterpret_cast<uint32_t*>(row + Geo::template word<kValue>(tok, c0)) = codes8(a, ga);
-  *reinterpret_cast<uint32_t*>(row + Geo::template word<kValue>(tok, c1)) = codes8(b, gb);
+  const Q4Place<D> at(slot, h, p.num_kv_heads, p.block_shift);
+  *reinterpret_cast<uint32_t*>(pool + at.row + Geo::template word<kValue>(at.tok, c0)) = codes8(a, ga);
+  *reinterpret_cast<uint32_t*>(pool + at.row + Geo::template word<kValue>(at.tok, c1)) = codes8(b, gb);
   const int group = kSplit ? item : (item & 3) == 0 ? item >> 2 : Geo::kGroups;
   if (group < Geo::kGroups)
-    *reinterpret_cast<uint32_t*>(sub + Geo::kCodeBytes + tok * Geo::kParamRow + group * 4) = mine;
+    *reinterpret_cast<uint32_t*>(pool + at.params + group * 4) = mine;
 }
 
 // grid.x walks tiles of tile_tokens tokens, grid.y slices of a tile's items.
-// kRotate: rotary_dim may be above 0.
-template <typename T, int D, bool kInterleaved, bool kQ4, bool kRotate>
+template <typename T, int D, bool kInterleaved, bool kQ4>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs p) {
   constexpr int N = VecOf<T>::N;
   constexpr int kItems = D / (2 * N);  // items (threads) of one head
-  constexpr bool kSplit = kRotate && !kInterleaved;
   extern __shared__ float2 cs[];       // [tile_tokens][rotary_dim / 2]
   const int tid = threadIdx.x;
   const int half = p.rotary_dim / 2;
@@ -262,7 +279,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
   for (int tile = blockIdx.x; tile * static_cast<int64_t>(p.tile_tokens) < p.num_tokens; tile += gridDim.x) {
     const int64_t tok0 = tile * static_cast<int64_t>(p.tile_tokens);
     const int nt = static_cast<int>(min(static_cast<int64_t>(p.tile_tokens), p.num_tokens - tok0));
-    for (int i = tid; kRotate && i < nt * half; i += kRopeThreads) {
+    for (int i = tid; i < nt * half; i += kRopeThreads) {
       const int t = i / half;
       const double u = static_cast<double>(p.positions[tok0 + t]) *
                        (static_cast<double>(p.inv_freq[i - t * half]) * 0.31830988618379067154);
@@ -270,7 +287,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
       sincospif(static_cast<float>(u - 2.0 * rint(0.5 * u)), &s, &c);
       cs[i] = make_float2(c * p.mscale, s * p.mscale);
     }
-    if (kRotate) __syncthreads();
+    __syncthreads();
 
     const int total = nt * heads * kItems;
     const int step = gridDim.y * kRopeThreads;
@@ -284,7 +301,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
         const int item = i % kItems, th = i / kItems;
         tk[u] = th / heads;
         hd[u] = th - tk[u] * heads;
-        const bool rotated = kRotate && item < rot_items && hd[u] < p.num_q_heads + p.num_kv_heads;
+        const bool rotated = item < rot_items && hd[u] < p.num_q_heads + p.num_kv_heads;
         c0[u] = !kInterleaved && rotated ? item : 2 * item;
         c1[u] = !kInterleaved && rotated ? item + rot_items : 2 * item + 1;
         if (i >= total) {
@@ -309,7 +326,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
         const int item = (base + u * step + tid) % kItems;
         const bool is_q = hd[u] >= 0 && hd[u] < p.num_q_heads;
         const bool is_v = hd[u] >= p.num_q_heads + p.num_kv_heads;
-        if (kRotate && hd[u] >= 0 && !is_v && item < rot_items)
+        if (hd[u] >= 0 && !is_v && item < rot_items)
           rotate<T, kInterleaved>(a[u], b[u], cs + tk[u] * half, item * N);
         const int64_t t = tok0 + tk[u];
         if (is_q) {
@@ -332,8 +349,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
           const bool any_k = __any_sync(0xffffffffu, slot >= 0 && !is_v);
           const bool any_v = __any_sync(0xffffffffu, slot >= 0 && is_v);
           if (any_k)
-            store_q4<D, false, kSplit>(static_cast<uint8_t*>(p.k_pool), a[u], b[u], c0[u], c1[u], item,
-                                       is_v ? -1 : slot, h, p);
+            store_q4<D, false, !kInterleaved>(static_cast<uint8_t*>(p.k_pool), a[u], b[u], c0[u], c1[u], item,
+                                              is_v ? -1 : slot, h, p);
           if (any_v)
             store_q4<D, true, false>(static_cast<uint8_t*>(p.v_pool), a[u], b[u], c0[u], c1[u], item,
                                      is_v ? slot : -1, h, p);
@@ -346,55 +363,116 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
         }
       }
     }
-    if (kRotate) __syncthreads();  // cs is rewritten for the next tile
+    __syncthreads();  // cs is rewritten for the next tile
   }
 }
 
-// Values of 4-bit rows. A thread takes the same eight dims of the same head of
-// K and of V in every token that it visits, kGatherUnroll tokens at a time, so
-// that only the slots differ; grid.x walks tokens, grid.y a token's octets.
-constexpr int kGatherThreads = 256, kGatherUnroll = 2;
+// How the plain 4-bit append and read spread a token's `per_token` items over
+// threads: a thread keeps its item (a piece of one head) in every token it
+// visits, so that only the slot changes and nothing is divided per token;
+// grid.x walks tokens, grid.y the items beyond a block's width.
+constexpr int kRowThreads = 256;
+struct RowShare {
+  int item;             // -1: this thread has none
+  int64_t first, step;  // its tokens: first, first + step, ...
+  __device__ __forceinline__ explicit RowShare(int per_token) {
+    const int width = min(per_token, kRowThreads), side = kRowThreads / width;
+    const int mine = threadIdx.x / width;
+    item = blockIdx.y * width + (threadIdx.x - mine * width);
+    if (mine >= side || item >= per_token) item = -1;
+    first = static_cast<int64_t>(blockIdx.x) * side + mine;
+    step = static_cast<int64_t>(gridDim.x) * side;
+  }
+};
+
+dim3 row_grid(int per_token, int64_t num_tokens, int tokens_per_thread) {
+  const int width = std::min(per_token, kRowThreads), side = kRowThreads / width;
+  const int64_t run = static_cast<int64_t>(side) * tokens_per_thread;
+  return dim3(static_cast<unsigned>(std::min<int64_t>((num_tokens + run - 1) / run, 1 << 30)),
+              static_cast<unsigned>((per_token + width - 1) / width));
+}
+
+// Quantises new rows: a thread takes the same 16 dims of K and of V; four
+// neighbouring threads hold a group.
+template <int D>
+__global__ void __launch_bounds__(kRowThreads)
+    kv_append_q4_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
+                        int64_t k_stride, int64_t v_stride, const int64_t* __restrict__ slots, int num_tokens,
+                        int num_kv_heads, int block_shift, int64_t num_slots, uint8_t* __restrict__ k_pool,
+                        uint8_t* __restrict__ v_pool, uint32_t* dev_err) {
+  using Geo = Q4Geo<D>;
+  constexpr int C = D / 16;
+  const RowShare sh(num_kv_heads * C);
+  if (sh.item < 0) return;  // (four neighbours leave together)
+  const uint32_t quad = 0xfu << (threadIdx.x & 28);
+  const int item = sh.item % C, h = sh.item / C;
+  for (int64_t t = sh.first; t < num_tokens; t += sh.step) {
+    const int64_t slot = slots[t];
+    const __nv_bfloat16* src[2] = {k_new + t * k_stride + sh.item * 16, v_new + t * v_stride + sh.item * 16};
+    Vec16 x[2][2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      x[kv][0] = load16(src[kv]);
+      x[kv][1] = load16(src[kv] + 8);
+    }
+    if (slot < 0) continue;
+    if (slot >= num_slots) {
+      if (sh.item == 0) report(dev_err, PA_DEVERR_SLOT);
+      continue;
+    }
+    const Q4Place<D> at(slot, h, num_kv_heads, block_shift);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint32_t s = min_bf16x2(spread8(x[kv][0]), spread8(x[kv][1]));
+      s = min_bf16x2(s, __shfl_xor_sync(quad, s, 1));
+      s = min_bf16x2(s, __shfl_xor_sync(quad, s, 2));
+      const Quant g = group_params(s);
+      uint8_t* pool = kv ? v_pool : k_pool;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = 2 * item + i;
+        const int word = kv ? Geo::v_word(at.tok, c) : Geo::k_word(at.tok, c);
+        *reinterpret_cast<uint32_t*>(pool + at.row + word) = codes8(x[kv][i], g);
+      }
+      if ((item & 3) == 0) *reinterpret_cast<uint32_t*>(pool + at.params + (item >> 2) * 4) = g.param;
+    }
+  }
+}
+
+// Values of 4-bit rows: a thread takes the same eight dims of K and of V,
+// kGatherUnroll tokens at a time.
+constexpr int kGatherUnroll = 2;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kGatherThreads)
+__global__ void __launch_bounds__(kRowThreads)
     kv_gather_q4_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
                         const int64_t* __restrict__ slots, int num_tokens, int num_kv_heads, int block_shift,
                         int64_t num_slots, T* __restrict__ k_out, T* __restrict__ v_out, uint32_t* dev_err) {
   using Geo = Q4Geo<D>;
   constexpr int C = D / 8;
-  const int per_token = num_kv_heads * C;
-  // tokens side by side in a block, and this thread's token and octet
-  const int width = min(per_token, kGatherThreads), side = kGatherThreads / width;
-  const int mine = threadIdx.x / width;
-  const int item = blockIdx.y * width + (threadIdx.x - mine * width);
-  if (mine >= side || item >= per_token) return;
-  const int c = item % C, h = item / C;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * side;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * side + mine; t0 < num_tokens; t0 += step * kGatherUnroll) {
+  const RowShare sh(num_kv_heads * C);
+  if (sh.item < 0) return;
+  const int c = sh.item % C, h = sh.item / C;
+  for (int64_t t0 = sh.first; t0 < num_tokens; t0 += sh.step * kGatherUnroll) {
     int64_t tok_at[kGatherUnroll];
     uint32_t w[kGatherUnroll][2], q[kGatherUnroll][2];
 #pragma unroll
     for (int u = 0; u < kGatherUnroll; ++u) {
-      const int64_t t = t0 + u * step;
+      const int64_t t = t0 + u * sh.step;
       tok_at[u] = -1;
       if (t >= num_tokens) continue;
       const int64_t slot = slots[t];
       if (slot < 0) continue;
       if (slot >= num_slots) {
-        if (item == 0) report(dev_err, PA_DEVERR_SLOT);
+        if (sh.item == 0) report(dev_err, PA_DEVERR_SLOT);
         continue;
       }
       tok_at[u] = t;
-      const int64_t blk = slot >> block_shift;
-      const int off = static_cast<int>(slot) & ((1 << block_shift) - 1);
-      const int tok = off & 15;
-      const int64_t sub = (((blk * num_kv_heads + h) << (block_shift - 4)) + (off >> 4)) * Geo::kSubBytes;
-      const int64_t row = sub + tok * Geo::kRowBytes;
-      const int64_t par = sub + Geo::kCodeBytes + tok * Geo::kParamRow + (c >> 3) * 4;
-      w[u][0] = *reinterpret_cast<const uint32_t*>(k_pool + row + Geo::k_word(tok, c));
-      w[u][1] = *reinterpret_cast<const uint32_t*>(v_pool + row + Geo::v_word(tok, c));
-      q[u][0] = *reinterpret_cast<const uint32_t*>(k_pool + par);
-      q[u][1] = *reinterpret_cast<const uint32_t*>(v_pool + par);
+      const Q4Place<D> at(slot, h, num_kv_heads, block_shift);
+      w[u][0] = *reinterpret_cast<const uint32_t*>(k_pool + at.row + Geo::k_word(at.tok, c));
+      w[u][1] = *reinterpret_cast<const uint32_t*>(v_pool + at.row + Geo::v_word(at.tok, c));
+      q[u][0] = *reinterpret_cast<const uint32_t*>(k_pool + at.params + (c >> 3) * 4);
+      q[u][1] = *reinterpret_cast<const uint32_t*>(v_pool + at.params + (c >> 3) * 4);
     }
 #pragma unroll
     for (int u = 0; u < kGatherUnroll; ++u) {
@@ -435,7 +513,7 @@ int sm_count() {
   return n;
 }
 
-template <typename T, int D, bool kInterleaved, bool kQ4, bool kRotate>
+template <typename T, int D, bool kInterleaved, bool kQ4>
 void launch_rope(RopeArgs p, cudaStream_t stream) {
   const int sms = sm_count();
   const int heads = p.num_q_heads + 2 * p.num_kv_heads;
@@ -452,15 +530,14 @@ void launch_rope(RopeArgs p, cudaStream_t stream) {
   // tiles and others with 3 at 16384 tokens.
   const int64_t gx = std::min<int64_t>(tiles, 1 << 30);
   const size_t smem = static_cast<size_t>(p.tile_tokens) * (p.rotary_dim / 2) * sizeof(float2);
-  rope_append_kernel<T, D, kInterleaved, kQ4, kRotate>
+  rope_append_kernel<T, D, kInterleaved, kQ4>
       <<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kRopeThreads, smem, stream>>>(p);
 }
 
 template <typename T, int D, bool kQ4>
 void pick_layout(const RopeArgs& p, bool interleaved, cudaStream_t stream) {
-  if (p.rotary_dim == 0) launch_rope<T, D, false, kQ4, false>(p, stream);
-  else if (interleaved) launch_rope<T, D, true, kQ4, true>(p, stream);
-  else launch_rope<T, D, false, kQ4, true>(p, stream);
+  if (interleaved) launch_rope<T, D, true, kQ4>(p, stream);
+  else launch_rope<T, D, false, kQ4>(p, stream);
 }
 
 template <typename T, bool kQ4>
@@ -468,6 +545,20 @@ void pick_dim(const RopeArgs& p, int head_dim, bool interleaved, cudaStream_t st
   if (head_dim == 64) pick_layout<T, 64, kQ4>(p, interleaved, stream);
   else if (head_dim == 128) pick_layout<T, 128, kQ4>(p, interleaved, stream);
   else pick_layout<T, 256, kQ4>(p, interleaved, stream);
+}
+
+template <int D>
+void launch_append(const RopeArgs& p, cudaStream_t stream) {
+  kv_append_q4_kernel<D><<<row_grid(p.num_kv_heads * (D / 16), p.num_tokens, 1), kRowThreads, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(p.k), static_cast<const __nv_bfloat16*>(p.v), p.k_stride, p.v_stride, p.slots,
+      p.num_tokens, p.num_kv_heads, p.block_shift, p.num_slots, static_cast<uint8_t*>(p.k_pool),
+      static_cast<uint8_t*>(p.v_pool), p.dev_err);
+}
+
+void pick_append(const RopeArgs& p, int head_dim, cudaStream_t stream) {
+  if (head_dim == 64) launch_append<64>(p, stream);
+  else if (head_dim == 128) launch_append<128>(p, stream);
+  else launch_append<256>(p, stream);
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -524,7 +615,8 @@ pa_status_t run_rope(RopeArgs p, int head_dim, bool interleaved, int num_blocks,
   }
   p.num_slots = static_cast<int64_t>(num_blocks) * p.block_size;
   p.block_shift = p.block_size == 16 ? 4 : 5;
-  if (q4) pick_dim<__nv_bfloat16, true>(p, head_dim, interleaved, stream);
+  if (q4 && p.num_q_heads == 0 && p.rotary_dim == 0) pick_append(p, head_dim, stream);
+  else if (q4) pick_dim<__nv_bfloat16, true>(p, head_dim, interleaved, stream);
   else if (dtype == PA_BF16) pick_dim<__nv_bfloat16, false>(p, head_dim, interleaved, stream);
   else pick_dim<float, false>(p, head_dim, interleaved, stream);
   const cudaError_t err = cudaGetLastError();
@@ -535,11 +627,7 @@ pa_status_t run_rope(RopeArgs p, int head_dim, bool interleaved, int num_blocks,
 template <typename T, int D>
 void launch_gather(const void* k_pool, const void* v_pool, const int64_t* slots, int T_, int H, int bs,
                    int64_t num_slots, void* k_out, void* v_out, uint32_t* err, cudaStream_t st) {
-  const int per_token = H * (D / 8), width = std::min(per_token, kGatherThreads), side = kGatherThreads / width;
-  const int gy = (per_token + width - 1) / width;
-  const int64_t gx = std::min<int64_t>((static_cast<int64_t>(T_) + side * kGatherUnroll - 1) / (side * kGatherUnroll), 1 << 30);
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
-  kv_gather_q4_kernel<T, D><<<grid, kGatherThreads, 0, st>>>(
+  kv_gather_q4_kernel<T, D><<<row_grid(H * (D / 8), T_, kGatherUnroll), kRowThreads, 0, st>>>(
       static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), slots, T_, H, bs == 16 ? 4 : 5, num_slots,
       static_cast<T*>(k_out), static_cast<T*>(v_out), err);
 }
