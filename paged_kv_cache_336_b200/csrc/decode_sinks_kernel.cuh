@@ -15,6 +15,10 @@ namespace pagedkv {
 
 struct SinksArgs : DecodeArgs {
   int num_sinks;  // first tokens that stay visible beside the window
+  // Lists per KV head: with fp32's CUDA-core math a KV head's group may be cut
+  // into several lists of fewer query heads (num_kv_heads and group are then
+  // those of the lists), each reading the head's K and V.
+  int head_tiles;
 };
 
 // A sliding window with sinks (the first a.num_sinks tokens stay visible): the
@@ -142,6 +146,7 @@ __global__ void __launch_bounds__(Cfg::kThreads)
   const int groups = static_cast<int>(gridDim.x) * W / Hkv;
   const int h = wg % Hkv;   // this warp's KV head
   const int gi = wg / Hkv;  // its group
+  const int kv_heads = Hkv / a.head_tiles, kv_head = h / a.head_tiles;  // of the pools
   const int C = max((U + groups - 1) / groups, (umax + a.max_pieces - 2) / (a.max_pieces - 1));
   const int64_t g_begin = static_cast<int64_t>(gi) * C;
   const int g0 = static_cast<int>(g_begin < U ? g_begin : U);
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(Cfg::kThreads)
     const int u = un < ns ? un : (fu & ~kSinkFlag) + un - ns;
     const int phys = a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + u / UPB];
     if (phys < 0 || phys >= a.num_blocks) return -2;
-    return (phys * Hkv + h) * BS + (u % UPB) * UR;
+    return (phys * kv_heads + kv_head) * BS + (u % UPB) * UR;
   };
 
   const uint64_t policy = l2_policy(a.l2_hint);

@@ -15,7 +15,8 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("dtype,G,bs,D", [
-    (workloads.F32, 1, 16, 128), (workloads.F32, 2, 32, 64), (workloads.BF16, 1, 32, 128),
+    (workloads.F32, 1, 16, 128), (workloads.F32, 2, 32, 64), (workloads.F32, 8, 16, 64),
+    (workloads.F32, 4, 32, 128), (workloads.BF16, 1, 32, 128),
     (workloads.BF16, 8, 16, 128), (workloads.BF16, 6, 16, 64), (workloads.BF16, 16, 32, 256)])
 @pytest.mark.parametrize("window,sinks", [(1, 1), (7, 4), (40, 16), (40, 17), (16, 37), (97, 0),
                                           (33, 150), (30, 5000), (10_000, 4)])
@@ -83,3 +84,20 @@ def test_long_contexts_many_pieces():
                                      w.scale, 9000, 1000)
     got = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, 9000, 1000)
     check_close(to_f64(got), want, workloads.BF16, "long")
+
+
+def test_fp32_groups_cut_or_whole():
+    """A group of 8 fp32 heads: few sequences (its heads dealt to several warps)
+    and the same ones inside a large batch (where they stay together)."""
+    w = workloads.random_small(31, num_seqs=400, num_q_heads=16, num_kv_heads=2, head_dim=64,
+                               block_size=16, dtype=workloads.F32, max_ctx=100,
+                               fixed_lens=[100, 64, 99])
+    bm, k_pool, v_pool = setup(w)
+    q = workloads.draw_queries(w, 400, device="cuda")
+    bt, ctx, tables, ctx_np = device_tables(bm, list(range(400)))
+    many = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, 40, 3)
+    few = binding.decode_split_sinks(q[:3], k_pool, v_pool, bt[:3], ctx[:3], w.scale, 40, 3)
+    want = oracle.paged_decode_sinks(to_f64(q[:3]), to_f64(k_pool), to_f64(v_pool), tables[:3], ctx_np[:3],
+                                     w.scale, 40, 3)
+    check_close(to_f64(few), want, workloads.F32, "few")
+    check_close(to_f64(many[:3]), want, workloads.F32, "many")
