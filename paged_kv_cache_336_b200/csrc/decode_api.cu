@@ -633,7 +633,7 @@ pa_status_t run_decode_q4(const DecodeReq& r, int window, int num_sinks, int par
   // Units of one list, at most: bounds the grid for small batches (with sinks
   // a sequence may list one unit twice).
   const int64_t units_max = static_cast<int64_t>(r.num_seqs) *
-                            ((static_cast<int64_t>(r.max_blocks_per_seq) * r.block_size + 15) / 16 + 1);
+                            ((static_cast<int64_t>(r.max_blocks_per_seq) * r.block_size + 15) / 16 + 1 + 8);
   if (units_max >= (int64_t(1) << 31))
     return fail(PA_ERR_UNSUPPORTED, "num_seqs * max context / 16 must be < 2^31");
 

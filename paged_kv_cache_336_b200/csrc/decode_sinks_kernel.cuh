@@ -36,12 +36,14 @@ __device__ __forceinline__ int sink_units(const SinksArgs& a, int first_unit) {
 // Every sequence's units: first_unit[B] (-1: nothing to read) and the exclusive
 // prefix sum prefix[B + 1], in shared memory, built by all threads of a CTA
 // of W warps; returns the number of units of each KV head's list and of the
-// longest sequence.
+// longest sequence. kPad places without units follow each sequence's units in
+// the list, so that an equal cut of the list also shares out what a sequence
+// costs besides its units.
 struct UnitLists {
   int total, longest;
 };
 
-template <int W>
+template <int W, int kPad = 0>
 __device__ __forceinline__ UnitLists build_unit_lists(const SinksArgs& a, int bs, int* prefix, int* first_unit) {
   constexpr int NT = 32 * W;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -65,7 +67,7 @@ __device__ __forceinline__ UnitLists build_unit_lists(const SinksArgs& a, int bs
       first_unit[i] = sinks_apart(a, ftok) ? ub | kSinkFlag : 0;
       u = sinks_apart(a, ftok) ? u + (a.num_sinks + 15) / 16 : (ctx + 15) / 16;
     }
-    mine += u;
+    mine += u + kPad;
     biggest = max(biggest, u);
   }
   int incl = mine;
@@ -87,7 +89,7 @@ __device__ __forceinline__ UnitLists build_unit_lists(const SinksArgs& a, int bs
     const int fu = first_unit[i];
     int u = 1;
     if (fu >= 0) u = (clamp_ctx(a.context_lens[i], max_tokens) + 15) / 16 - (fu & ~kSinkFlag) + sink_units(a, fu);
-    run += u;
+    run += u + kPad;
   }
   if (tid == NT - 1) prefix[B] = base + incl;
   __syncthreads();
