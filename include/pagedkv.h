@@ -467,10 +467,12 @@ pa_status_t pa_kv_gather_q4(const void* k_pool, const void* v_pool, const int64_
  * for. q and out bf16 (dtype PA_BF16), any group size 1..16, head_dim 64, 128
  * or 256. num_sinks without a window changes nothing.
  *
- * Arithmetic: logits in fp32 from products of bf16 queries with the codes
- * (exact integers); softmax weights times the values' scales are rounded to
- * bf16 before the product with the value codes, as P is in the bf16 path;
- * minima enter in fp32. Key and value scales up to 2^100.
+ * Arithmetic: queries enter as 16-bit whole numbers relative to the largest
+ * |q| of their head (off by at most 2^-15 of it), multiplied with the codes
+ * exactly; logits, softmax sums and minima are fp32; softmax weights times the
+ * values' scales are rounded to f16 (11 bits) before the product with the
+ * value codes. Key scales up to 2^100; value scales up to 2^61, and below
+ * 2^-54 with fewer than 11 bits.
  *
  * workspace, partition_tokens: the contract of pa_decode_split with the same
  * sizes; the work is cut as for its long tables (equal runs of 16-token

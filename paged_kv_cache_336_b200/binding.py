@@ -671,7 +671,8 @@ def rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_pool, v_po
     _check(fn(q_ptr, k_new.data_ptr(), v_new.data_ptr(), q_stride,
               _token_rows(k_new, Hkv, D, "k_new"), _token_rows(v_new, Hkv, D, "v_new"),
               positions.data_ptr(), inv_freq.data_ptr(), slot_mapping.data_ptr(), T, Hq, Hkv, D,
-              2 * inv_freq.size(0), 1 if interleaved else 0, mscale, BS, NB, _dtype_code(k_new),
+              2 * inv_freq.size(0), 1 if interleaved else 0, float(mscale), BS, NB,
+              _dtype_code(k_new),
               out_ptr, k_pool.data_ptr(), v_pool.data_ptr(), _ptr(dev_err), _stream_ptr(stream)))
     return q_out if q is not None else None
 

@@ -216,8 +216,9 @@ pa_status_t validate_and_pick(const DecodeReq& r, DecodeInstance* inst) {
 
 // Optional host-side check of the device tables (PAGEDKV_VALIDATE=1): copies
 // block tables and context lengths to the host and checks every entry the
-// kernels will read. Synchronous; meant for tests and debugging.
-pa_status_t host_validate(const DecodeReq& r) {
+// kernels will read (with a window, those of blocks that hold a visible token).
+// Synchronous; meant for tests and debugging.
+pa_status_t host_validate(const DecodeReq& r, int window = 0, int num_sinks = 0) {
   static const bool enabled = [] {
     const char* e = std::getenv("PAGEDKV_VALIDATE");
     return e != nullptr && e[0] == '1';
@@ -234,6 +235,8 @@ pa_status_t host_validate(const DecodeReq& r) {
       return fail(PA_ERR_INVALID_ARG, "context_lens[%d] = %d out of range", s, ctx[s]);
     const int nb = (ctx[s] + r.block_size - 1) / r.block_size;
     for (int i = 0; i < nb; ++i) {
+      const int64_t first = static_cast<int64_t>(i) * r.block_size;
+      if (window > 0 && first + r.block_size <= static_cast<int64_t>(ctx[s]) - window && first >= num_sinks) continue;
       const int32_t b = bt[static_cast<size_t>(s) * r.max_blocks_per_seq + i];
       if (b < 0 || b >= r.num_blocks)
         return fail(PA_ERR_INVALID_ARG, "block_tables[%d][%d] = %d out of range", s, i, b);
@@ -423,7 +426,7 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
   pa_status_t st = validate_and_pick(r, &inst);
   if (st != PA_OK) return st;
   if (r.num_seqs == 0) return ok();
-  st = host_validate(r);
+  st = host_validate(r, extras != nullptr ? extras->window : 0, extras != nullptr ? extras->num_sinks : 0);
   if (st != PA_OK) return st;
 
   SinksArgs a{};  // the kernels without sinks take its DecodeArgs part
@@ -630,6 +633,8 @@ pa_status_t run_decode_q4(const DecodeReq& r, int window, int num_sinks, int par
                                      partition_tokens);
   if (workspace_bytes < L.total)
     return fail(PA_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", workspace_bytes, L.total);
+  st = host_validate(r, window, num_sinks);
+  if (st != PA_OK) return st;
   // Units of one list, at most: bounds the grid for small batches (with sinks
   // a sequence may list one unit twice).
   const int64_t units_max = static_cast<int64_t>(r.num_seqs) *

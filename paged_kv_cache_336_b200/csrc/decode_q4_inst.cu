@@ -20,9 +20,11 @@ static DecodeInstance make_q4() {
 }
 
 // Consumer warps x units a step x ring slots (of a step's K or V). Measured at
-// head_dim 128 on 8 x 131072 tokens / 256 ragged sequences: 12 x 4 x 3 260 /
-// 107 us; 12 x 3 x 4 275 / 109; 8 x 4 x 4 274 / 112; 12 x 2 x 4 307 / 124 (per-
-// step work over fewer units). head_dim 256 needs 232 registers: 8 warps.
+// head_dim 128 on 8 x 131072 tokens / 256 ragged sequences, before the lists'
+// padding: 12 x 4 x 3 260 / 107 us; 12 x 3 x 4 275 / 109; 8 x 4 x 4 274 / 112;
+// 12 x 2 x 4 307 / 124 (per-step work over fewer units). A fourth slot gains
+// 1.5% and leaves no room for the lists of 4096 sequences. head_dim 256 needs
+// 232 registers: 8 warps.
 template <int BS>
 static bool pick(int head_dim, DecodeInstance* out) {
   if (head_dim == 64) { *out = make_q4<BS, 64, 12, 4, 4>(); return true; }

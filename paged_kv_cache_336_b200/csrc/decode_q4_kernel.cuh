@@ -11,29 +11,43 @@
 // relative to 8, so that what is summed over a long context stays near zero.
 //
 // How.
-// * Work is cut as in paged_decode_stream_kernel: one list of 16-token units
-//   per KV head (per 8 query heads of it where a group has more), every warp
-//   of a persistent grid an equal run of its list, pieces merged by
+// * Work is cut as in paged_decode_sinks_kernel: one list of 16-token units per
+//   KV head (per 8 query heads of it where a group has more), every consumer
+//   warp of a persistent grid an equal run of its list, pieces merged by
 //   lse_merge_kernel. A unit is one sub-tile of K and of V, 9 head_dim bytes
-//   each and contiguous: two bulk copies into the warp's ring.
-// * mma.sync m16n8k16 with the 16 tokens of a unit as the rows and 8 query
-//   heads as the columns, both times: S = K Q^T, O^T = V^T P^T. A group of 8
-//   heads then wastes no row (with heads as rows half would be padding).
-//   Fragments come straight from the code words: which dims (or tokens) stand
-//   at which k index is free as long as both operands agree, so the words
-//   are stored in the order the lanes want them, and no ldmatrix or shuffle
-//   is needed. Row r of S is token r / 2 (r even), 7 - r / 2 (odd), + 8 for
-//   r >= 8: the rows that lanes read together then lie in different banks.
-// * A code becomes bf16 128 + c by one mask-or of two codes in place: (w >> 4j)
-//   & 0x000f000f | 0x43004300. The 128 is taken out by the accumulators'
-//   start: -128 Q_i for S, and -136 sum p s (a product with a constant row,
-//   so that it is the same rounded numbers) for O. Accumulators of O start
-//   afresh each step and are added to the running O in fp32, which bounds
-//   what that cancellation can cost.
-// * P is scaled by s, rounded to bf16 (as P is in the 16-bit kernel), and
-//   transposed between its two layouts by movmatrix.
-// Bound: HBM by bytes (4.5 bits a value), with the integer pipe close behind:
-// about 0.9 mask, shift and permute instructions a value.
+//   each and contiguous: one bulk copy each.
+// * Four producer warps keep the consumers' rings full (eight lanes per
+//   consumer, one unit each), because a warp that fills its own ring spends
+//   74 of its 330 instructions a unit on that; registers are split by
+//   setmaxnreg, 160 a consumer thread and 32 a producer one with 12 consumers.
+// * mma.sync with the 16 tokens of a unit as the rows and 8 query heads as the
+//   columns, both times: S = K Q^T, O^T = V^T P^T. A group of 8 heads then wastes
+//   no row (with heads as rows half would be padding). Fragments come straight
+//   from the code words: which dims (or tokens) stand at which k index is free
+//   as long as both operands agree, so the words are stored in the order the
+//   lanes want them, and no ldmatrix or shuffle is needed. Row r of S is token
+//   r / 2 (r even) or 7 - r / 2 (odd), + 8 for r >= 8: the rows that lanes read
+//   together then lie in different banks.
+// * S: codes as bytes (a mask of the word and of the word >> 4) against q as
+//   rint(2^k q), 16 bits in two bytes, k bringing the head's largest |q| into
+//   [2^14, 2^15): u8 x s8 and u8 x u8 products of depth 32 with exact 32-bit
+//   sums. Against bf16 operands (128 + c by a mask-or) that is 3 integer
+//   instructions for 8 codes instead of 7. e4m3 products, whose bytes 0..15 are
+//   c / 512 exactly, measured slower: without native hardware behind mma.sync
+//   they cost conversions and two f16 products each.
+// * O: codes less 8 as f16 (CodeBits) against p s in f16, transposed between
+//   its two layouts by movmatrix. f16 needs the weights' range bounded: see
+//   Q4Warp::expo. In exchange O accumulates in place, where a mask-or'ed bf16
+//   code (128 + c) would leave a cancellation of 128 to a few.
+// * Steps of 64 tokens share one running maximum; the accumulators are rescaled
+//   only when it (or expo) moves. Steps that are not whole go unit by unit
+//   through the masked build.
+// Rounding: q to 16 bits of its head's range (at most 2^-15 of the largest),
+// p s to f16 (2^-11), the output to bf16; sums, logits, minima in fp32 or exact.
+// Bound: 8 x 131072 tokens (64 heads over 8, head_dim 128) take 256 us, 1.21 GB
+// at 4.7 TB/s, 0.72 of the measured copy rate. Copies alone take 203 us and the
+// math alone 214 us; together they draw 1000 W, the GPU's limit, at 1.86 GHz.
+// Integer pipe 52% busy, issue slots 60%.
 #pragma once
 
 #include <climits>
@@ -466,7 +480,9 @@ struct Q4Warp {
   }
   __device__ __forceinline__ void store_partial(const DecodeArgs& a, int64_t pr, int h, int g) const {
     if (g == 0) {
-      a.part_m[pr] = m[h];
+      // a piece without a token (bad block ids) weighs nothing; -inf would make
+      // the merge of nothing but such pieces a NaN
+      a.part_m[pr] = m[h] == -INFINITY ? kNoTokens : m[h];
       a.part_l[pr] = l[h];
     }
 #pragma unroll

@@ -13,6 +13,10 @@
 
 namespace pagedkv {
 
+// Running maximum of a piece in which no token was found (every block id bad),
+// for the merge: finite, below any logit.
+constexpr float kNoTokens = -1e30f;
+
 struct SinksArgs : DecodeArgs {
   int num_sinks;  // first tokens that stay visible beside the window
   // Lists per KV head: with fp32's CUDA-core math a KV head's group may be cut
@@ -267,6 +271,8 @@ __global__ void __launch_bounds__(Cfg::kThreads)
         T* o = reinterpret_cast<T*>(a.out) + row0 * D;
         st.store_final(o + g * D, o + (g + 8) * D, g < G, g + 8 < G, lane);
       } else {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) st.m[r] = st.m[r] == -INFINITY ? kNoTokens : st.m[r];
         const int64_t pr0 = g < G ? (row0 + g) * a.max_partitions + piece : -1;
         const int64_t pr1 = g + 8 < G ? (row0 + g + 8) * a.max_partitions + piece : -1;
         st.store_partials(a, pr0, pr1, lane);
@@ -275,6 +281,8 @@ __global__ void __launch_bounds__(Cfg::kThreads)
       if (whole) {
         st.store_final(reinterpret_cast<T*>(a.out) + row0 * D, lane);
       } else {
+#pragma unroll
+        for (int r = 0; r < WarpT::G; ++r) st.m[r] = st.m[r] == -INFINITY ? kNoTokens : st.m[r];
         st.store_partials(a, row0 * a.max_partitions + piece, a.max_partitions, lane);
       }
     }

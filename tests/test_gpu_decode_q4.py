@@ -215,3 +215,75 @@ def test_workspace_is_reused_and_results_repeat():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, a)
+
+
+def test_a_long_sequence_of_bad_blocks_gives_zeros():
+    """Every block id outside the pool, the work cut into many pieces: zeros and
+    the error bit, beside an untouched neighbour."""
+    q, k, v, tables, lens = make(16, [3000, 40], 4, 2, 64, 16)
+    args = [torch.from_numpy(x).cuda() for x in (k, v, tables, lens)]
+    want = binding.decode_q4(q.cuda(), *args, 0.1, partition_tokens=32)
+    args[2][0] = 10 ** 6
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = binding.decode_q4(q.cuda(), *args, 0.1, partition_tokens=32, dev_err=err)
+    assert int(err.item()) == binding.DEVERR_BLOCK_ID
+    assert torch.all(got[0] == 0) and torch.equal(got[1], want[1])
+
+
+def test_the_most_sequences():
+    rng = np.random.default_rng(17)
+    lens = rng.integers(0, 20, 4096).tolist()
+    check(*make(17, lens, 1, 1, 64, 16), 16)
+
+
+def test_scales_that_grow_and_a_nan_beside_them():
+    """Value scales over 2^-30 .. 2^30, rising along the sequence; then a NaN
+    scale in one group, which leaves the other group's dims as they were."""
+    q, k, v, tables, lens = make(18, [333, 200], 4, 1, 128, 16)
+    sub = v.reshape(v.shape[0], 1, 9 * 128)
+    for s in range(2):
+        for b in range(-(-int(lens[s]) // 16)):
+            par = np.ascontiguousarray(sub[tables[s, b], 0, 1024:]).view(np.uint16).reshape(16, 2, 2)
+            val = so.bf16_value(par) * 2.0 ** (-30 + 60 * b / 21)
+            sub[tables[s, b], 0, 1024:] = so.bf16_bits(val).reshape(-1).view(np.uint8)
+    want = check(q, k, v, tables, lens, 16, scale=0.02)
+    sub[tables[0, 3], 0, 1024 + 8 * 5:1024 + 8 * 5 + 4] = 0xff       # token 53, dims 0 .. 63
+    args = [torch.from_numpy(x).cuda() for x in (k, v, tables, lens)]
+    got = binding.decode_q4(q.cuda(), *args, 0.02, partition_tokens=64)
+    assert torch.isnan(got[0, :, :64]).all() and torch.equal(got[0, :, 64:], want[0, :, 64:])
+    assert torch.equal(got[1], want[1])
+
+
+def test_offsets_past_32_bits():
+    """Pools of more than 4 GiB, sequences in their last blocks: append, read
+    back, attention, and rope_append into 16-bit pools of that size."""
+    D, H, bs = 256, 8, 32
+    NB = (1 << 32) // (H * 9 * D * 2) + 200
+    kp, vp = (torch.empty(NB, H, 2 * 9 * D, dtype=torch.uint8, device="cuda") for _ in range(2))
+    T = 100
+    g = torch.Generator(device="cuda").manual_seed(19)
+    k, v = (torch.randn(T, H, D, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(1, H, D, device="cuda", generator=g).to(torch.bfloat16)
+    blocks = torch.arange(NB - 1, NB - 5, -1, device="cuda")
+    slots = (blocks[:, None] * bs + torch.arange(bs, device="cuda")).flatten()[:T]
+    binding.kv_append_q4(k, v, slots, kp, vp)
+    small = [torch.empty(4, H, 2 * 9 * D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    near = torch.arange(T, device="cuda")
+    binding.kv_append_q4(k, v, near, *small)
+    for a, b in zip(binding.kv_gather_q4(kp, vp, slots, D), binding.kv_gather_q4(*small, near, D)):
+        assert torch.equal(a, b)
+    ctx = torch.tensor([T], dtype=torch.int32, device="cuda")
+    a = binding.decode_q4(q, kp, vp, blocks.to(torch.int32)[None], ctx, 0.06)
+    b = binding.decode_q4(q, *small, torch.arange(4, dtype=torch.int32, device="cuda")[None], ctx, 0.06)
+    assert torch.equal(a, b)
+    del kp, vp
+    NB = (1 << 32) // (H * bs * D * 2) + 100
+    kp = torch.empty(NB, H, bs, D, dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    slots = torch.arange(NB * bs - T, NB * bs, device="cuda")
+    inv, m = binding.rope_frequencies(D)
+    binding.rope_append(None, k, v, torch.zeros(T, dtype=torch.int32, device="cuda"), inv, slots, kp, vp, mscale=m)
+    rows = vp[-4:].transpose(1, 2).reshape(-1, H, D)[-T:]
+    assert torch.equal(rows, v)
+    rows = kp[-4:].transpose(1, 2).reshape(-1, H, D)[-T:]
+    assert torch.equal(rows, k)                       # position 0: nothing turns

@@ -54,7 +54,7 @@ def call(tables, lens, new, queue, state, bs, max_tokens, err=None):
 CASES = [
     ([5], [1], 16, 1), ([16], [1], 16, 4), ([0], [0], 16, 0), ([0, 0], [40, 33], 16, 80),
     ([15, 16, 17, 0, 31], [1, 1, 1, 1, 1], 16, 9), ([3, 40, 7], [-1, 5, -1], 16, 5),
-    ([64, 64], [-1, -1], 32, 3), ([1] * 300, [1] * 300, 16, 301),
+    ([64, 64], [-1, -1], 32, 3), ([], [], 16, 0), ([], [], 16, 6), ([7], [0], 16, 3), ([1] * 300, [1] * 300, 16, 301),
 ]
 
 

@@ -101,3 +101,60 @@ def test_fp32_groups_cut_or_whole():
                                      w.scale, 40, 3)
     check_close(to_f64(few), want, workloads.F32, "few")
     check_close(to_f64(many[:3]), want, workloads.F32, "many")
+
+
+@pytest.mark.parametrize("dtype", [workloads.F32, workloads.BF16])
+def test_bad_blocks_give_zeros_and_spare_the_neighbour(dtype):
+    w = workloads.random_small(91, num_seqs=2, num_q_heads=4, num_kv_heads=2, head_dim=64, block_size=16,
+                               dtype=dtype, max_ctx=900, fixed_lens=[900, 70])
+    bm, k_pool, v_pool = setup(w)
+    q = workloads.draw_queries(w, 2, device="cuda")
+    bt, ctx, _, _ = device_tables(bm, [0, 1])
+    want = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, 500, 20, partition_tokens=16)
+    bt[0] = 10 ** 6
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, 500, 20, partition_tokens=16, dev_err=err)
+    assert int(err.item()) == binding.DEVERR_BLOCK_ID
+    assert torch.all(got[0] == 0) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [workloads.F32, workloads.BF16])
+def test_many_sequences(dtype):
+    w = workloads.random_small(92, num_seqs=4096, num_q_heads=1, num_kv_heads=1, head_dim=64, block_size=16,
+                               dtype=dtype, max_ctx=40, fixed_lens=[0, 40, 33])
+    bm, k_pool, v_pool = setup(w)
+    q = workloads.draw_queries(w, 4096, device="cuda")
+    bt, ctx, tables, ctx_np = device_tables(bm, list(range(4096)))
+    want = oracle.paged_decode_sinks(to_f64(q), to_f64(k_pool), to_f64(v_pool), tables, ctx_np, w.scale, 9, 3)
+    got = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, 9, 3)
+    check_close(to_f64(got), want, dtype, "4096 sequences")
+
+
+def test_host_validation_looks_at_visible_blocks_only():
+    """PAGEDKV_VALIDATE=1 (read once per process): tables with released blocks pass
+    a windowed call, a bad visible block is refused."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from paged_kv_cache_336_b200 import binding
+q = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+k, v = binding.q4_pools(8, 1, 16, 64)
+t = torch.tensor([[0, -1, -1, 2, 3]], dtype=torch.int32, device="cuda")
+c = torch.tensor([70], dtype=torch.int32, device="cuda")
+kk = torch.zeros(8, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+binding.decode_q4(q, k, v, t, c, 0.1, window=20, sinks=3)
+binding.decode_split_sinks(q, kk, kk, t, c, 0.1, 20, 3)
+for f in (lambda: binding.decode_q4(q, k, v, t, c, 0.1), lambda: binding.decode_split_sinks(q, kk, kk, t, c, 0.1, 40, 3)):
+    try:
+        f()
+    except binding.InvalidArgumentError:
+        continue
+    raise SystemExit("a bad block was accepted")
+torch.cuda.synchronize()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], env={**os.environ, "PAGEDKV_VALIDATE": "1", "PYTHONPATH": root},
+                       cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
