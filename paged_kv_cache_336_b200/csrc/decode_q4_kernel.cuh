@@ -50,8 +50,6 @@
 // Integer pipe 52% busy, issue slots 60%.
 #pragma once
 
-#include <climits>
-
 #include "decode_sinks_kernel.cuh"
 #include "q4_common.cuh"
 
@@ -505,7 +503,8 @@ struct Q4Run {
 };
 
 template <class Cfg>
-__device__ __forceinline__ Q4Run q4_run(const SinksArgs& a, const UnitLists& lists, int q_tiles, int warp) {
+__device__ __forceinline__ Q4Run q4_run(const SinksArgs& a, const UnitLists& lists, const int* prefix, int q_tiles,
+                                        int warp) {
   const int num_lists = a.num_kv_heads * q_tiles;
   const int wg = static_cast<int>(blockIdx.x) * Cfg::W + warp;
   const int groups = static_cast<int>(gridDim.x) * Cfg::W / num_lists;
@@ -513,6 +512,12 @@ __device__ __forceinline__ Q4Run q4_run(const SinksArgs& a, const UnitLists& lis
   r.h = (wg % num_lists) / q_tiles;  // KV head
   r.qt = wg % q_tiles;               // run of its query heads
   r.gi = wg / num_lists;
+  if (a.whole_seqs) {
+    r.C = INT_MAX;
+    r.g0 = prefix[min(r.gi, a.num_seqs)];
+    r.g1 = prefix[min(r.gi + 1, a.num_seqs)];
+    return r;
+  }
   r.C = max((lists.total + groups - 1) / groups, (lists.longest + a.max_pieces - 2) / (a.max_pieces - 1));
   const int64_t total = lists.total, begin = static_cast<int64_t>(r.gi) * r.C;
   r.g0 = static_cast<int>(min(begin, total));
@@ -541,7 +546,7 @@ __device__ __forceinline__ void q4_produce(const uint8_t* k_pool, const uint8_t*
   constexpr int US = Cfg::US, NS = Cfg::NS, UPB = Cfg::UPB;
   const int lane = threadIdx.x & 31, u = lane & 7;
   const int c = which + 4 * (lane >> 3);
-  Q4Run run = q4_run<Cfg>(a, lists, q_tiles, min(c, Cfg::W - 1));
+  Q4Run run = q4_run<Cfg>(a, lists, prefix, q_tiles, min(c, Cfg::W - 1));
   if (c >= Cfg::W) run.g1 = run.g0;
   const int g1 = run.g1, h = run.h;
   ring += (min(c, Cfg::W - 1) * NS) * Cfg::kSlotBytes + u * Geo::kSubBytes;
@@ -653,7 +658,7 @@ __device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, cons
   constexpr int US = Cfg::US, NS = Cfg::NS, D = Cfg::D;
   constexpr uint32_t kUnitMask = (1u << US) - 1u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Q4Run run = q4_run<Cfg>(a, lists, q_tiles, warp);
+  const Q4Run run = q4_run<Cfg>(a, lists, prefix, q_tiles, warp);
   const int g0 = run.g0, g1 = run.g1, h = run.h, C = run.C;
   if (g0 >= g1) return;
   const uint32_t my_ring = smem_addr(ring) + warp * NS * Cfg::kSlotBytes;

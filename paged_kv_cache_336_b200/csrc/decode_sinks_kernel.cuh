@@ -9,6 +9,8 @@
 // units and then the window's, so that no other block is read.
 #pragma once
 
+#include <climits>
+
 #include "decode_stream_kernel.cuh"
 
 namespace pagedkv {
@@ -23,6 +25,9 @@ struct SinksArgs : DecodeArgs {
   // into several lists of fewer query heads (num_kv_heads and group are then
   // those of the lists), each reading the head's K and V.
   int head_tiles;
+  // Non-zero: warp number w takes the whole of sequence w / lists of list w %
+  // lists (a grid of as many warps), so that no merge follows.
+  int whole_seqs;
 };
 
 // A sliding window with sinks (the first a.num_sinks tokens stay visible): the
@@ -153,10 +158,12 @@ __global__ void __launch_bounds__(Cfg::kThreads)
   const int h = wg % Hkv;   // this warp's KV head
   const int gi = wg / Hkv;  // its group
   const int kv_heads = Hkv / a.head_tiles, kv_head = h / a.head_tiles;  // of the pools
-  const int C = max((U + groups - 1) / groups, (umax + a.max_pieces - 2) / (a.max_pieces - 1));
-  const int64_t g_begin = static_cast<int64_t>(gi) * C;
+  const int C = a.whole_seqs ? INT_MAX
+                             : max((U + groups - 1) / groups, (umax + a.max_pieces - 2) / (a.max_pieces - 1));
+  const int64_t g_begin = a.whole_seqs ? prefix[min(gi, B)] : static_cast<int64_t>(gi) * C;
+  const int64_t g_end = a.whole_seqs ? prefix[min(gi + 1, B)] : g_begin + C;
   const int g0 = static_cast<int>(g_begin < U ? g_begin : U);
-  const int g1 = static_cast<int>(g_begin + C < U ? g_begin + C : U);
+  const int g1 = static_cast<int>(g_end < U ? g_end : U);
   const int nj = gi < groups ? g1 - g0 : 0;
   if (nj <= 0) return;
 
@@ -262,7 +269,7 @@ __global__ void __launch_bounds__(Cfg::kThreads)
   };
   // Writes the segment out: final rows when this warp covered all of it, else the partial slot of this warp's piece.
   auto end_segment = [&](bool reached_end) {
-    const int piece = gi - seg_start / C;
+    const int piece = a.whole_seqs ? 0 : gi - seg_start / C;
     const bool whole = reached_end && seg_start >= g0;
     const int64_t row0 = static_cast<int64_t>(s) * a.num_q_heads + static_cast<int64_t>(h) * G;
     if constexpr (Cfg::kMma) {

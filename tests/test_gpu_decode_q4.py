@@ -287,3 +287,13 @@ def test_offsets_past_32_bits():
     assert torch.equal(rows, v)
     rows = kp[-4:].transpose(1, 2).reshape(-1, H, D)[-T:]
     assert torch.equal(rows, k)                       # position 0: nothing turns
+
+
+@pytest.mark.parametrize("num,Hkv", [(1, 1), (7, 5), (300, 2), (1200, 3)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 3)])
+def test_short_sequences_whole_and_cut(num, Hkv, window, sinks):
+    """Sequences of at most eight units: one warp each while a wave of CTAs holds
+    them, an equal cut beyond."""
+    rng = np.random.default_rng(num)
+    lens = [127, 0][:num] + rng.integers(0, 128, max(0, num - 2)).tolist()
+    check(*make(num, lens, 2 * Hkv, Hkv, 128, 16, slack=0), 16, window, sinks)

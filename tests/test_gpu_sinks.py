@@ -158,3 +158,17 @@ torch.cuda.synchronize()
     r = subprocess.run([sys.executable, "-c", code], env={**os.environ, "PAGEDKV_VALIDATE": "1", "PYTHONPATH": root},
                        cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("num", [1, 9, 900])
+def test_short_windows_whole_and_cut(num):
+    """Windows of a few units: one warp a sequence while a wave of CTAs holds
+    them, an equal cut beyond."""
+    w = workloads.random_small(95 + num, num_seqs=num, num_q_heads=16, num_kv_heads=4, head_dim=64, block_size=16,
+                               dtype=workloads.BF16, max_ctx=130, fixed_lens=[130, 60, 61][:num])
+    bm, k_pool, v_pool = setup(w)
+    q = workloads.draw_queries(w, num, device="cuda")
+    bt, ctx, tables, ctx_np = device_tables(bm, list(range(num)))
+    want = oracle.paged_decode_sinks(to_f64(q), to_f64(k_pool), to_f64(v_pool), tables, ctx_np, w.scale, 50, 9)
+    got = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, 50, 9)
+    check_close(to_f64(got), want, workloads.BF16, "short windows")
