@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(Cfg::kThreads)
       if (lane == 0) a.seg_pieces[static_cast<int64_t>(s) * Hkv + h] = pieces;
     }
   };
-  // Writes the segment out: final rows when this warp covered all of it, else the partial slot of this warp's piece.
+  // Writes the segment out: final rows when this warp covered all of it, else
+  // the partial slot of this warp's piece.
   auto end_segment = [&](bool reached_end) {
     const int piece = a.whole_seqs ? 0 : gi - seg_start / C;
     const bool whole = reached_end && seg_start >= g0;

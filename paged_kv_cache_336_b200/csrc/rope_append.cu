@@ -599,6 +599,8 @@ pa_status_t run_rope(RopeArgs p, int head_dim, bool interleaved, int num_blocks,
   if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.q_out) || !aligned16(p.k_pool) ||
       !aligned16(p.v_pool))
     return fail(PA_ERR_INVALID_ARG, "q, k_new, v_new, q_out and pools must be 16-byte aligned");
+  if (q4 && static_cast<int64_t>(p.num_kv_heads) * head_dim >= (int64_t(1) << 24))  // (the append's grid.y)
+    return fail(PA_ERR_UNSUPPORTED, "too many heads");
   // One item's indices are 32-bit.
   if (4 * (static_cast<int64_t>(p.num_q_heads) + 2 * static_cast<int64_t>(p.num_kv_heads)) * 32 >= (int64_t(1) << 30))
     return fail(PA_ERR_UNSUPPORTED, "too many heads");
