@@ -50,6 +50,8 @@
 // Integer pipe 52% busy, issue slots 60%.
 #pragma once
 
+#include <climits>
+
 #include "decode_sinks_kernel.cuh"
 #include "q4_common.cuh"
 
@@ -512,7 +514,7 @@ __device__ __forceinline__ Q4Run q4_run(const SinksArgs& a, const UnitLists& lis
   r.h = (wg % num_lists) / q_tiles;  // KV head
   r.qt = wg % q_tiles;               // run of its query heads
   r.gi = wg / num_lists;
-  if (a.whole_seqs) {
+  if (a.seq_cut == 1) {
     r.C = INT_MAX;
     r.g0 = prefix[min(r.gi, a.num_seqs)];
     r.g1 = prefix[min(r.gi + 1, a.num_seqs)];

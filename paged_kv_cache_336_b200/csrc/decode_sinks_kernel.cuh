@@ -9,8 +9,6 @@
 // units and then the window's, so that no other block is read.
 #pragma once
 
-#include <climits>
-
 #include "decode_stream_kernel.cuh"
 
 namespace pagedkv {
@@ -25,9 +23,10 @@ struct SinksArgs : DecodeArgs {
   // into several lists of fewer query heads (num_kv_heads and group are then
   // those of the lists), each reading the head's K and V.
   int head_tiles;
-  // Non-zero: warp number w takes the whole of sequence w / lists of list w %
-  // lists (a grid of as many warps), so that no merge follows.
-  int whole_seqs;
+  // Non-zero: each sequence's units are cut into so many equal pieces, and warp
+  // number w takes piece w / lists % cut of sequence w / lists / cut of list w %
+  // lists (a grid of as many warps). 1: whole sequences, and no merge follows.
+  int seq_cut;
 };
 
 // A sliding window with sinks (the first a.num_sinks tokens stay visible): the
@@ -158,10 +157,14 @@ __global__ void __launch_bounds__(Cfg::kThreads)
   const int h = wg % Hkv;   // this warp's KV head
   const int gi = wg / Hkv;  // its group
   const int kv_heads = Hkv / a.head_tiles, kv_head = h / a.head_tiles;  // of the pools
-  const int C = a.whole_seqs ? INT_MAX
-                             : max((U + groups - 1) / groups, (umax + a.max_pieces - 2) / (a.max_pieces - 1));
-  const int64_t g_begin = a.whole_seqs ? prefix[min(gi, B)] : static_cast<int64_t>(gi) * C;
-  const int64_t g_end = a.whole_seqs ? prefix[min(gi + 1, B)] : g_begin + C;
+  int C = max((U + groups - 1) / groups, (umax + a.max_pieces - 2) / (a.max_pieces - 1));
+  int64_t g_begin = static_cast<int64_t>(gi) * C, g_end = g_begin + C;
+  if (a.seq_cut > 0) {
+    const int seq = min(gi / a.seq_cut, B - 1), units = prefix[seq + 1] - prefix[seq];
+    C = (units + a.seq_cut - 1) / a.seq_cut;
+    g_begin = prefix[seq] + static_cast<int64_t>(gi % a.seq_cut) * C;
+    g_end = gi < B * a.seq_cut ? min(g_begin + C, static_cast<int64_t>(prefix[seq + 1])) : g_begin;
+  }
   const int g0 = static_cast<int>(g_begin < U ? g_begin : U);
   const int g1 = static_cast<int>(g_end < U ? g_end : U);
   const int nj = gi < groups ? g1 - g0 : 0;
@@ -263,14 +266,14 @@ __global__ void __launch_bounds__(Cfg::kThreads)
       st.begin(q_group, a.scale_log2, lane);
     }
     if (un == 0) {  // this warp holds the segment's first piece: record the count
-      const int pieces = (seg_start + us - 1) / C - seg_start / C + 1;
+      const int pieces = a.seq_cut > 0 ? (us + C - 1) / C : (seg_start + us - 1) / C - seg_start / C + 1;
       if (lane == 0) a.seg_pieces[static_cast<int64_t>(s) * Hkv + h] = pieces;
     }
   };
   // Writes the segment out: final rows when this warp covered all of it, else
   // the partial slot of this warp's piece.
   auto end_segment = [&](bool reached_end) {
-    const int piece = a.whole_seqs ? 0 : gi - seg_start / C;
+    const int piece = a.seq_cut > 0 ? gi % a.seq_cut : gi - seg_start / C;
     const bool whole = reached_end && seg_start >= g0;
     const int64_t row0 = static_cast<int64_t>(s) * a.num_q_heads + static_cast<int64_t>(h) * G;
     if constexpr (Cfg::kMma) {

@@ -172,3 +172,20 @@ def test_short_windows_whole_and_cut(num):
     want = oracle.paged_decode_sinks(to_f64(q), to_f64(k_pool), to_f64(v_pool), tables, ctx_np, w.scale, 50, 9)
     got = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, 50, 9)
     check_close(to_f64(got), want, workloads.BF16, "short windows")
+
+
+@pytest.mark.parametrize("dtype,Hq", [(workloads.F32, 8), (workloads.BF16, 12)])
+@pytest.mark.parametrize("window,sinks", [(700, 4), (33, 0), (20, 700), (5000, 1)])
+@pytest.mark.parametrize("partition_tokens", [512, 1024])
+def test_sequences_cut_one_by_one(dtype, Hq, window, sinks, partition_tokens):
+    """Tables of up to three partitions: each sequence is cut by itself into equal
+    pieces, some of them empty for short sequences."""
+    w = workloads.random_small(97, num_seqs=6, num_q_heads=Hq, num_kv_heads=2, head_dim=64, block_size=32,
+                               dtype=dtype, max_ctx=1400, fixed_lens=[1400, 0, 1, 17, 70, 1399])
+    bm, k_pool, v_pool = setup(w)
+    q = workloads.draw_queries(w, 6, device="cuda")
+    bt, ctx, tables, ctx_np = device_tables(bm, list(range(6)))
+    want = oracle.paged_decode_sinks(to_f64(q), to_f64(k_pool), to_f64(v_pool), tables, ctx_np, w.scale, window, sinks)
+    got = binding.decode_split_sinks(q, k_pool, v_pool, bt, ctx, w.scale, window, sinks,
+                                     partition_tokens=partition_tokens)
+    check_close(to_f64(got), want, dtype, "cut one by one")
