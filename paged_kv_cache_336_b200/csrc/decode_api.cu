@@ -435,7 +435,8 @@ constexpr int64_t kWholeUnits16 = 3;
 // that pieces have to be longest / (max_pieces - 1) units; where a workspace
 // holds this few pieces, cutting each sequence by itself into max_pieces makes
 // them shorter. 7 sequences, fp32: 18.0 -> 12.3 us at a window of 97, 49.6 ->
-// 28.2 at 600; bf16 13.9 -> 10.5.
+// 28.2 at 600; bf16 13.9 -> 10.5; the 4-bit kernel, 7 and 30 sequences of up to
+// 700 tokens: 30.3 -> 19.6 and 30.8 -> 19.9.
 constexpr int kAlignedPieces = 4;
 
 // clear_header: zero the workspace's control header on r.stream right before
@@ -714,11 +715,10 @@ pa_status_t run_decode_q4(const DecodeReq& r, int window, int num_sinks, int par
   const int64_t W = inst.warps, lists = static_cast<int64_t>(r.num_kv_heads) * q_tiles;
   const int64_t need = (units_max * lists + W - 1) / W, at_least = (lists + W - 1) / W;
   int64_t ctas = std::max(at_least, std::min<int64_t>(need, static_cast<int64_t>(dinfo.sms) * occ));
-  const int64_t each = (static_cast<int64_t>(r.num_seqs) * lists + W - 1) / W;
-  if (each <= static_cast<int64_t>(dinfo.sms) * occ && most_units(r, window, num_sinks) <= kWholeUnits) {
-    a.seq_cut = 1;
-    ctas = each;
-  }
+  const int64_t wave = static_cast<int64_t>(dinfo.sms) * occ, seq_lists = static_cast<int64_t>(r.num_seqs) * lists;
+  if (most_units(r, window, num_sinks) <= kWholeUnits && seq_lists <= wave * W) a.seq_cut = 1;
+  else if (a.max_pieces <= kAlignedPieces && seq_lists * a.max_pieces <= wave * W) a.seq_cut = a.max_pieces;
+  if (a.seq_cut > 0) ctas = (seq_lists * a.seq_cut + W - 1) / W;
   const void *kp = r.k_pool, *vp = r.v_pool;
   void* args[] = {&kp, &vp, &q_tiles, &a};
   const cudaError_t err = cudaLaunchKernel(inst.kernel, dim3(static_cast<unsigned>(ctas)), dim3(inst.threads), args,

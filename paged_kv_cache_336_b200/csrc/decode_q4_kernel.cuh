@@ -514,10 +514,11 @@ __device__ __forceinline__ Q4Run q4_run(const SinksArgs& a, const UnitLists& lis
   r.h = (wg % num_lists) / q_tiles;  // KV head
   r.qt = wg % q_tiles;               // run of its query heads
   r.gi = wg / num_lists;
-  if (a.seq_cut == 1) {
-    r.C = INT_MAX;
-    r.g0 = prefix[min(r.gi, a.num_seqs)];
-    r.g1 = prefix[min(r.gi + 1, a.num_seqs)];
+  if (a.seq_cut > 0) {  // each sequence by itself
+    const int seq = min(r.gi / a.seq_cut, a.num_seqs - 1), end = prefix[seq + 1] - kQ4Pad;
+    r.C = (end - prefix[seq] + a.seq_cut - 1) / a.seq_cut;
+    r.g0 = min(prefix[seq] + r.gi % a.seq_cut * r.C, end);
+    r.g1 = r.gi < a.num_seqs * a.seq_cut ? min(r.g0 + r.C, end) : r.g0;
     return r;
   }
   r.C = max((lists.total + groups - 1) / groups, (lists.longest + a.max_pieces - 2) / (a.max_pieces - 1));
@@ -696,18 +697,20 @@ __device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, cons
     }
     st.begin(row, g < heads, a.scale_log2, lane);
     if (seg0 >= g0 && run.qt == 0 && lane == 0)  // the first piece's warp records how many there are
-      a.seg_pieces[static_cast<int64_t>(s) * a.num_kv_heads + h] = (seg1 - 1) / C - seg0 / C + 1;
+      a.seg_pieces[static_cast<int64_t>(s) * a.num_kv_heads + h] =
+          a.seq_cut > 0 ? (seg1 - seg0 + C - 1) / C : (seg1 - 1) / C - seg0 / C + 1;
   };
   auto end_segment = [&]() {
     st.finish();
     const bool whole = seg0 >= g0 && seg1 <= g1;
+    const int piece = a.seq_cut > 0 ? run.gi % a.seq_cut : run.gi - seg0 / C;
     const int64_t row0 = static_cast<int64_t>(s) * a.num_q_heads + head0;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (2 * t + e >= heads) continue;
       const int64_t row = row0 + 2 * t + e;
       if (whole) st.store_final(static_cast<__nv_bfloat16*>(a.out) + row * D, e, g);
-      else st.store_partial(a, row * a.max_partitions + run.gi - seg0 / C, e, g);
+      else st.store_partial(a, row * a.max_partitions + piece, e, g);
     }
   };
 
