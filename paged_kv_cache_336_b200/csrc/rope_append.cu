@@ -394,6 +394,7 @@ dim3 row_grid(int per_token, int64_t num_tokens, int tokens_per_thread) {
 
 // Quantises new rows: a thread takes the same 16 dims of K and of V; four
 // neighbouring threads hold a group.
+constexpr int kAppendCtasPerSm = 3;  // 70 to 78 registers; measured 41.1 us (with the read) against 45.4 for 4, 43.3 for 12
 template <int D>
 __global__ void __launch_bounds__(kRowThreads)
     kv_append_q4_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
@@ -406,15 +407,23 @@ __global__ void __launch_bounds__(kRowThreads)
   if (sh.item < 0) return;  // (four neighbours leave together)
   const uint32_t quad = 0xfu << (threadIdx.x & 28);
   const int item = sh.item % C, h = sh.item / C;
+  Vec16 next[2][2];
+  int64_t next_slot = -1;
+  auto load = [&](int64_t t) {  // the next token's rows, while this one's are quantised
+    if (t >= num_tokens) return;
+    next_slot = slots[t];
+    const __nv_bfloat16* k = k_new + t * k_stride + sh.item * 16;
+    const __nv_bfloat16* v = v_new + t * v_stride + sh.item * 16;
+    next[0][0] = load16(k);
+    next[0][1] = load16(k + 8);
+    next[1][0] = load16(v);
+    next[1][1] = load16(v + 8);
+  };
+  load(sh.first);
   for (int64_t t = sh.first; t < num_tokens; t += sh.step) {
-    const int64_t slot = slots[t];
-    const __nv_bfloat16* src[2] = {k_new + t * k_stride + sh.item * 16, v_new + t * v_stride + sh.item * 16};
-    Vec16 x[2][2];
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      x[kv][0] = load16(src[kv]);
-      x[kv][1] = load16(src[kv] + 8);
-    }
+    const Vec16 x[2][2] = {{next[0][0], next[0][1]}, {next[1][0], next[1][1]}};
+    const int64_t slot = next_slot;
+    load(t + sh.step);
     if (slot < 0) continue;
     if (slot >= num_slots) {
       if (sh.item == 0) report(dev_err, PA_DEVERR_SLOT);
@@ -549,7 +558,10 @@ void pick_dim(const RopeArgs& p, int head_dim, bool interleaved, cudaStream_t st
 
 template <int D>
 void launch_append(const RopeArgs& p, cudaStream_t stream) {
-  kv_append_q4_kernel<D><<<row_grid(p.num_kv_heads * (D / 16), p.num_tokens, 1), kRowThreads, 0, stream>>>(
+  // As many CTAs as are resident, each walking its tokens a load ahead.
+  dim3 grid = row_grid(p.num_kv_heads * (D / 16), p.num_tokens, 1);
+  grid.x = std::min<unsigned>(grid.x, std::max<unsigned>(1u, kAppendCtasPerSm * sm_count() / grid.y));
+  kv_append_q4_kernel<D><<<grid, kRowThreads, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(p.k), static_cast<const __nv_bfloat16*>(p.v), p.k_stride, p.v_stride, p.slots,
       p.num_tokens, p.num_kv_heads, p.block_shift, p.num_slots, static_cast<uint8_t*>(p.k_pool),
       static_cast<uint8_t*>(p.v_pool), p.dev_err);
