@@ -44,10 +44,11 @@
 //   through the masked build.
 // Rounding: q to 16 bits of its head's range (at most 2^-15 of the largest),
 // p s to f16 (2^-11), the output to bf16; sums, logits, minima in fp32 or exact.
-// Bound: 8 x 131072 tokens (64 heads over 8, head_dim 128) take 256 us, 1.21 GB
-// at 4.7 TB/s, 0.72 of the measured copy rate. Copies alone take 203 us and the
-// math alone 214 us; together they draw 1000 W, the GPU's limit, at 1.86 GHz.
-// Integer pipe 52% busy, issue slots 60%.
+// Bound: 8 x 131072 tokens (64 heads over 8, head_dim 128) take 250 us, 1.21 GB
+// at 4.8 TB/s, 0.74 of the measured copy rate, and 280 us once the GPU has
+// reached its 1000 W limit (1.86 GHz), after some 100 ms of such calls. Copies
+// alone take 203 us and the math alone 214 us. Integer pipe 53% busy, issue
+// slots 61%.
 #pragma once
 
 #include <climits>

@@ -6,7 +6,11 @@
 // t >= ctx - window or t < num_sinks. How: paged_decode_stream_kernel's cut
 // (every warp of a persistent grid an equal run of a KV head's list of 16-token
 // units, pieces merged by lse_merge_kernel), over lists that hold the sinks'
-// units and then the window's, so that no other block is read.
+// units and then the window's, so that no other block is read; short windows
+// and small tables are cut sequence by sequence (SinksArgs::seq_cut).
+// Bound: 8 sequences of 100,000 to 131,072 tokens, window 4096 + 4, 64 heads
+// over 8 in bf16: 30.1 us (floor 20.6): 14 units a warp behind the launch, the
+// lists and the first loads, then the merge.
 #pragma once
 
 #include "decode_stream_kernel.cuh"

@@ -21,7 +21,9 @@
 // block takes its id from the queue, not from the table, and the queue's
 // read and written places are disjoint because count + returned <= cap.
 // Bound: launch latency and three dependent global round trips for a decode
-// step; 12 bytes a token for a prefill wave.
+// step (256 sequences 5.2 us); for a prefill wave the sums and table reads that
+// every CTA repeats, then 12 bytes a token (512 sequences, 465,000 tokens, some
+// sequences leaving: 10.3 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>

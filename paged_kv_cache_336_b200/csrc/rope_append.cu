@@ -26,7 +26,8 @@
 // puts its cos and sin in shared memory (one pair a thread, so that all heads
 // of a token share them) and walks the tile's items, each thread loading
 // kUnroll items before it uses any. Bound: HBM (each element read and written
-// once); for a decode step, launch latency.
+// once): 16384 tokens of 32 + 8 + 8 heads of 128 in bf16 take 68.4 us, 0.90 of
+// the measured copy rate; for a decode step, launch latency (one token 2.6 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -393,7 +394,8 @@ dim3 row_grid(int per_token, int64_t num_tokens, int tokens_per_thread) {
 }
 
 // Quantises new rows: a thread takes the same 16 dims of K and of V; four
-// neighbouring threads hold a group.
+// neighbouring threads hold a group. About 10 instructions an element beside
+// 2.6 bytes moved: 16384 rows of 8 heads of 128 take 21 us (floor 13).
 constexpr int kAppendCtasPerSm = 3;  // 70 to 78 registers; measured 41.1 us (with the read) against 45.4 for 4, 43.3 for 12
 template <int D>
 __global__ void __launch_bounds__(kRowThreads)
@@ -449,7 +451,9 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // Values of 4-bit rows: a thread takes the same eight dims of K and of V,
-// kGatherUnroll tokens at a time.
+// kGatherUnroll tokens at a time (16384 rows of 8 heads of 128 with their
+// append: 43.4 us for one, 41.0 for two, 41.3 for four). Bound: the 16-bit
+// stores, behind a slot and then a row load.
 constexpr int kGatherUnroll = 2;
 
 template <typename T, int D>
