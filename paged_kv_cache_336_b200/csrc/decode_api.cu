@@ -423,20 +423,17 @@ int64_t most_units(const DecodeReq& r, int window, int num_sinks) {
   return std::min<int64_t>(all, (static_cast<int64_t>(window) + 15) / 16 + 1 + (static_cast<int64_t>(num_sinks) + 15) / 16);
 }
 
-// Sequences of at most this many units go to one warp each and need no merge,
-// where one wave of CTAs holds them all. Measured on the 4-bit kernel, 8 lists,
-// sequences of up to 110 tokens: 11.3 us against 14.5 for 64 of them, 12.4
-// against 19.2 for 200, but 54.5 against 50.9 for 1000 (several waves); a
-// call's host time falls by 2 us.
-constexpr int64_t kWholeUnits = 8;
-// 16-bit windows with sinks: the same for fewer units, each taking a warp longer.
+// 4-bit decode: where one wave of CTAs holds every sequence cut into k pieces of
+// at most this many units, k a divisor of a CTA's consumers, they are merged
+// in the CTA (k = 1: not at all) and no merge kernel follows.
+constexpr int64_t kPieceUnits = 16;
+// 16-bit windows with sinks of at most this many units: a warp each and no merge.
 constexpr int64_t kWholeUnits16 = 3;
 // An equal cut of a whole list leaves a sequence's ends wherever they fall, so
 // that pieces have to be longest / (max_pieces - 1) units; where a workspace
 // holds this few pieces, cutting each sequence by itself into max_pieces makes
 // them shorter. 7 sequences, fp32: 18.0 -> 12.3 us at a window of 97, 49.6 ->
-// 28.2 at 600; bf16 13.9 -> 10.5; the 4-bit kernel, 7 and 30 sequences of up to
-// 700 tokens: 30.3 -> 19.6 and 30.8 -> 19.9.
+// 28.2 at 600; bf16 13.9 -> 10.5.
 constexpr int kAlignedPieces = 4;
 
 // clear_header: zero the workspace's control header on r.stream right before
@@ -716,15 +713,23 @@ pa_status_t run_decode_q4(const DecodeReq& r, int window, int num_sinks, int par
   const int64_t need = (units_max * lists + W - 1) / W, at_least = (lists + W - 1) / W;
   int64_t ctas = std::max(at_least, std::min<int64_t>(need, static_cast<int64_t>(dinfo.sms) * occ));
   const int64_t wave = static_cast<int64_t>(dinfo.sms) * occ, seq_lists = static_cast<int64_t>(r.num_seqs) * lists;
-  if (most_units(r, window, num_sinks) <= kWholeUnits && seq_lists <= wave * W) a.seq_cut = 1;
-  else if (a.max_pieces <= kAlignedPieces && seq_lists * a.max_pieces <= wave * W) a.seq_cut = a.max_pieces;
-  if (a.seq_cut > 0) ctas = (seq_lists * a.seq_cut + W - 1) / W;
+  // As many pieces as a wave holds, but no more than make one step (4 units) each.
+  const int64_t most = most_units(r, window, num_sinks);
+  for (int64_t k = 1; k <= W; ++k) {
+    const int64_t each = W % k == 0 ? (seq_lists + W / k - 1) / (W / k) : wave + 1;
+    if (each > wave) continue;
+    if ((most + k - 1) / k <= kPieceUnits) {
+      a.seq_cut = static_cast<int>(k);
+      ctas = each;
+    }
+    if ((most + k - 1) / k <= 4) break;
+  }
   const void *kp = r.k_pool, *vp = r.v_pool;
   void* args[] = {&kp, &vp, &q_tiles, &a};
   const cudaError_t err = cudaLaunchKernel(inst.kernel, dim3(static_cast<unsigned>(ctas)), dim3(inst.threads), args,
                                            smem, r.stream);
   if (err != cudaSuccess) return fail(PA_ERR_CUDA, "decode_q4 launch: %s", cudaGetErrorString(err));
-  if (a.seq_cut != 1) {
+  if (a.seq_cut == 0) {
     st = launch_merge(inst.merge, r, a);
     if (st != PA_OK) return st;
   }

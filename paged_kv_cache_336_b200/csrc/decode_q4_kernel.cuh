@@ -500,28 +500,35 @@ struct Q4Warp {
 // 105 us for 0, 97.3 for 2, 95.1 for 4, 98.7 for 8.
 constexpr int kQ4Pad = 4;
 
-// What a warp has to do: units [g0, g1) of list (h, qt).
+// What a warp has to do: units [g0, g1) of list (h, qt); with seq_cut, as piece
+// `piece` of sequence `seq` (num_seqs and up: nothing).
 struct Q4Run {
-  int g0, g1, gi, h, qt, C;
+  int g0, g1, gi, h, qt, C, seq, piece;
 };
 
 template <class Cfg>
 __device__ __forceinline__ Q4Run q4_run(const SinksArgs& a, const UnitLists& lists, const int* prefix, int q_tiles,
                                         int warp) {
   const int num_lists = a.num_kv_heads * q_tiles;
+  Q4Run r{};
+  if (a.seq_cut > 0) {  // each sequence by itself
+    const int item = static_cast<int>(blockIdx.x) * (Cfg::W / a.seq_cut) + warp / a.seq_cut, list = item % num_lists;
+    r.h = list / q_tiles;
+    r.qt = list % q_tiles;
+    r.seq = item / num_lists;
+    r.piece = warp % a.seq_cut;
+    if (r.seq >= a.num_seqs) return r;
+    const int end = prefix[r.seq + 1] - kQ4Pad;
+    r.C = (end - prefix[r.seq] + a.seq_cut - 1) / a.seq_cut;
+    r.g0 = min(prefix[r.seq] + r.piece * r.C, end);
+    r.g1 = min(r.g0 + r.C, end);
+    return r;
+  }
   const int wg = static_cast<int>(blockIdx.x) * Cfg::W + warp;
   const int groups = static_cast<int>(gridDim.x) * Cfg::W / num_lists;
-  Q4Run r;
   r.h = (wg % num_lists) / q_tiles;  // KV head
   r.qt = wg % q_tiles;               // run of its query heads
   r.gi = wg / num_lists;
-  if (a.seq_cut > 0) {  // each sequence by itself
-    const int seq = min(r.gi / a.seq_cut, a.num_seqs - 1), end = prefix[seq + 1] - kQ4Pad;
-    r.C = (end - prefix[seq] + a.seq_cut - 1) / a.seq_cut;
-    r.g0 = min(prefix[seq] + r.gi % a.seq_cut * r.C, end);
-    r.g1 = r.gi < a.num_seqs * a.seq_cut ? min(r.g0 + r.C, end) : r.g0;
-    return r;
-  }
   r.C = max((lists.total + groups - 1) / groups, (lists.longest + a.max_pieces - 2) / (a.max_pieces - 1));
   const int64_t total = lists.total, begin = static_cast<int64_t>(r.gi) * r.C;
   r.g0 = static_cast<int>(min(begin, total));
@@ -654,15 +661,15 @@ __device__ __forceinline__ void q4_produce(const uint8_t* k_pool, const uint8_t*
   }
 }
 
+// Walks a consumer's run; with seq_cut above 1 it leaves the run's state in `st`.
 template <class Cfg>
-__device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, const UnitLists& lists, const int* prefix,
-                                           const int* first_unit, const uint8_t* ring, uint64_t* full, uint64_t* empty,
-                                           const uint32_t* present) {
+__device__ __forceinline__ void q4_walk(const SinksArgs& a, const Q4Run& run, Q4Warp<Cfg>& st, const int* prefix,
+                                        const int* first_unit, const uint8_t* ring, uint64_t* full, uint64_t* empty,
+                                        const uint32_t* present) {
   using Geo = typename Cfg::Geo;
   constexpr int US = Cfg::US, NS = Cfg::NS, D = Cfg::D;
   constexpr uint32_t kUnitMask = (1u << US) - 1u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Q4Run run = q4_run<Cfg>(a, lists, prefix, q_tiles, warp);
   const int g0 = run.g0, g1 = run.g1, h = run.h, C = run.C;
   if (g0 >= g1) return;
   const uint32_t my_ring = smem_addr(ring) + warp * NS * Cfg::kSlotBytes;
@@ -670,8 +677,6 @@ __device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, cons
   empty += warp * NS;
   present += warp * NS;
 
-  Q4Warp<Cfg> st;
-  st.places(lane);
   const int g = lane >> 2, t = lane & 3;
   const int heads = min(8, a.group - 8 * run.qt);
   const int head0 = h * a.group + 8 * run.qt;
@@ -697,21 +702,19 @@ __device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, cons
       for (int b = 0; b < D * 2; b += 128) prefetch_l2(nq + b);
     }
     st.begin(row, g < heads, a.scale_log2, lane);
-    if (seg0 >= g0 && run.qt == 0 && lane == 0)  // the first piece's warp records how many there are
-      a.seg_pieces[static_cast<int64_t>(s) * a.num_kv_heads + h] =
-          a.seq_cut > 0 ? (seg1 - seg0 + C - 1) / C : (seg1 - 1) / C - seg0 / C + 1;
+    if (a.seq_cut == 0 && seg0 >= g0 && run.qt == 0 && lane == 0)  // the first piece's warp records how many there are
+      a.seg_pieces[static_cast<int64_t>(s) * a.num_kv_heads + h] = (seg1 - 1) / C - seg0 / C + 1;
   };
   auto end_segment = [&]() {
     st.finish();
     const bool whole = seg0 >= g0 && seg1 <= g1;
-    const int piece = a.seq_cut > 0 ? run.gi % a.seq_cut : run.gi - seg0 / C;
     const int64_t row0 = static_cast<int64_t>(s) * a.num_q_heads + head0;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (2 * t + e >= heads) continue;
       const int64_t row = row0 + 2 * t + e;
       if (whole) st.store_final(static_cast<__nv_bfloat16*>(a.out) + row * D, e, g);
-      else st.store_partial(a, row * a.max_partitions + piece, e, g);
+      else st.store_partial(a, row * a.max_partitions + run.gi - seg0 / C, e, g);
     }
   };
 
@@ -733,6 +736,7 @@ __device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, cons
   begin_segment();
   for (;;) {
     if (cg == min(seg1, g1)) {
+      if (a.seq_cut > 1) return;
       end_segment();
       cg = prefix[++s];
       if (cg >= g1) return;
@@ -773,6 +777,69 @@ __device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, cons
       give();
     }
     cg += n;
+  }
+}
+
+template <class Cfg>
+__device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, const UnitLists& lists, const int* prefix,
+                                           const int* first_unit, uint8_t* ring, uint64_t* full, uint64_t* empty,
+                                           const uint32_t* present) {
+  constexpr int D = Cfg::D, W = Cfg::W;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Q4Run run = q4_run<Cfg>(a, lists, prefix, q_tiles, warp);
+  Q4Warp<Cfg> st;
+  st.places(lane);
+  st.m[0] = st.m[1] = -INFINITY;
+  q4_walk<Cfg>(a, run, st, prefix, first_unit, ring, full, empty, present);
+  if (a.seq_cut <= 1) return;
+  // ---- pieces of one sequence, merged in shared memory: every consumer comes
+  // here, with or without units. A warp's state takes the place of its ring,
+  // whose last copies it has used. ------------------------------------------------
+  constexpr int kState = 8 * (D + 2);  // values [8 heads][D], m [8], l [8]
+  static_assert(kState * 4 <= Cfg::NS * Cfg::kSlotBytes, "a warp's state fits its ring");
+  auto state = [&](int w) { return reinterpret_cast<float*>(ring + w * Cfg::NS * Cfg::kSlotBytes); };
+  const int g = lane >> 2, t = lane & 3;
+  float* mine = state(warp);
+  const bool some = run.g0 < run.g1;
+  if (some) st.finish();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (some) {
+#pragma unroll
+      for (int i = 0; i < Cfg::Geo::kGroups; ++i) {
+        float4* dst = reinterpret_cast<float4*>(mine + (2 * t + e) * D + 64 * i + 8 * g);
+        dst[0] = make_float4(st.value(i, e, 0), st.value(i, e, 1), st.value(i, e, 2), st.value(i, e, 3));
+        dst[1] = make_float4(st.value(i, e, 4), st.value(i, e, 5), st.value(i, e, 6), st.value(i, e, 7));
+      }
+    }
+    if (g == 0) {
+      mine[8 * D + 2 * t + e] = st.m[e];
+      mine[8 * D + 8 + 2 * t + e] = some ? st.l[e] : 0.f;
+    }
+  }
+  named_bar_sync(1, 32 * W);
+  if (run.seq >= a.num_seqs) return;
+  const int heads = min(8, a.group - 8 * run.qt), w0 = warp - run.piece;
+  for (int hd = run.piece; hd < heads; hd += a.seq_cut) {
+    float top = -INFINITY;
+    for (int p = 0; p < a.seq_cut; ++p) top = fmaxf(top, state(w0 + p)[8 * D + hd]);
+    float sum = 0.f, acc[D / 32];
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
+    for (int p = 0; p < a.seq_cut; ++p) {
+      const float* from = state(w0 + p);
+      const float pm = from[8 * D + hd];
+      if (pm == -INFINITY) continue;  // (no token: nothing was written)
+      const float wt = fast_exp2(pm - top);
+      sum = fmaf(from[8 * D + 8 + hd], wt, sum);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(from[hd * D + 2 * lane + 64 * (j / 2) + (j & 1)], wt, acc[j]);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t row = static_cast<int64_t>(run.seq) * a.num_q_heads + run.h * a.group + 8 * run.qt + hd;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row * D);
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) out[lane + 32 * j] = pack_bf16x2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
   }
 }
 

@@ -30,6 +30,8 @@ struct SinksArgs : DecodeArgs {
   // Non-zero: each sequence's units are cut into so many equal pieces, and warp
   // number w takes piece w / lists % cut of sequence w / lists / cut of list w %
   // lists (a grid of as many warps). 1: whole sequences, and no merge follows.
+  // The 4-bit kernel's pieces are neighbouring warps of one CTA, a divisor of
+  // its consumers, and are merged there.
   int seq_cut;
 };
 
