@@ -277,10 +277,9 @@ pa_status_t pa_decode_split_window(const void* q, const void* k_pool, const void
  * stay visible beside the window, so the query attends to tokens t < ctx with
  * t >= ctx - window or t < num_sinks (window >= 1, num_sinks >= 0). Blocks
  * that hold neither a sink nor a token of the window are never read and their
- * table entries may be -1. fp32 and bf16, the shapes of pa_decode_split; runs
- * on the balanced kernel whatever the table size (the partitions of the other
- * cut are runs of consecutive blocks). Same workspace and contract as
- * pa_decode_split.
+ * table entries may be -1. fp32 and bf16, the shapes of pa_decode_split. Large
+ * batches are cut as pa_decode_split cuts long tables, small ones sequence by
+ * sequence. Same workspace and contract as pa_decode_split.
  * ------------------------------------------------------------------------- */
 pa_status_t pa_decode_split_sinks(const void* q, const void* k_pool, const void* v_pool,
                                   const int32_t* block_tables, const int32_t* context_lens,
@@ -475,8 +474,9 @@ pa_status_t pa_kv_gather_q4(const void* k_pool, const void* v_pool, const int64_
  * 2^-54 with fewer than 11 bits.
  *
  * workspace, partition_tokens: the contract of pa_decode_split with the same
- * sizes; the work is cut as for its long tables (equal runs of 16-token
- * units), whatever the table size. num_seqs <= 4096.
+ * sizes; large batches are cut as for its long tables (equal runs of 16-token
+ * units), whatever the table size, small ones sequence by sequence. num_seqs <=
+ * 4096.
  * ------------------------------------------------------------------------- */
 pa_status_t pa_decode_q4(const void* q, const void* k_pool, const void* v_pool,
                          const int32_t* block_tables, const int32_t* context_lens, int num_seqs,

@@ -423,18 +423,39 @@ int64_t most_units(const DecodeReq& r, int window, int num_sinks) {
   return std::min<int64_t>(all, (static_cast<int64_t>(window) + 15) / 16 + 1 + (static_cast<int64_t>(num_sinks) + 15) / 16);
 }
 
-// 4-bit decode: where one wave of CTAs holds every sequence cut into k pieces of
-// at most this many units, k a divisor of a CTA's consumers, they are merged
-// in the CTA (k = 1: not at all) and no merge kernel follows.
-constexpr int64_t kPieceUnits = 16;
-// 16-bit windows with sinks of at most this many units: a warp each and no merge.
-constexpr int64_t kWholeUnits16 = 3;
-// An equal cut of a whole list leaves a sequence's ends wherever they fall, so
-// that pieces have to be longest / (max_pieces - 1) units; where a workspace
-// holds this few pieces, cutting each sequence by itself into max_pieces makes
-// them shorter. 7 sequences, fp32: 18.0 -> 12.3 us at a window of 97, 49.6 ->
-// 28.2 at 600; bf16 13.9 -> 10.5.
-constexpr int kAlignedPieces = 4;
+// How a batch's lists of units are cut: in equal runs (a.seq_cut stays 0; pieces
+// merged by the merge kernel), or each sequence by itself into a.seq_cut
+// pieces for neighbouring warps that merge in their CTA, without that kernel
+// (*ctas then). The latter where one wave of CTAs (`wave`, of W warps each)
+// holds every sequence of every list cut into k pieces, k a divisor of W, as
+// large as fits but no larger than makes pieces of `enough` units; if a piece
+// has at most kPieceUnits units, and at most kMergeUnits more than an equal run
+// would have (by the longest that a table or window allows). Measured, equal
+// runs against this: 4-bit, 8 lists, sequences of up to 700 tokens: 30.3
+// against 9.9 us for 7 of them, 30.8 against 12.9 for 30, 26.4 against 22.2 for
+// 100; 16 of up to 6000: 34.3 against 31.6 (pieces of up to 16 or 64 units were
+// slower); but 24.9 against 26.7 for 8 windows of 4096. fp32 windows with sinks,
+// 7 sequences: 18.0 against 7.2 at a window of 97, 49.6 against 15.9 at 600;
+// bf16 13.9 against 5.6; but 71 against 80 for 64 fp32 windows of 1000, whose
+// units take CUDA cores several times as long. A call's host time falls by 2 us.
+constexpr int64_t kPieceUnits = 32;
+constexpr int64_t kMergeUnits = 8;
+void cut_sequences(const DecodeReq& r, int64_t lists, int64_t most, int64_t W, int64_t wave, int64_t enough, SinksArgs* a,
+                   int64_t* ctas) {
+  const int64_t groups = std::max<int64_t>(1, wave * W / lists);
+  const int64_t run = std::max((r.num_seqs * most + groups - 1) / groups,
+                               (most + a->max_pieces - 2) / (a->max_pieces - 1));
+  for (int64_t k = 1; k <= W; ++k) {
+    const int64_t each = W % k == 0 ? (r.num_seqs * lists + W / k - 1) / (W / k) : wave + 1;
+    if (each > wave) continue;
+    const int64_t piece = (most + k - 1) / k;
+    if (piece <= kPieceUnits && piece <= run + (r.dtype == PA_F32 ? 0 : kMergeUnits)) {
+      a->seq_cut = static_cast<int>(k);
+      *ctas = each;
+    }
+    if (piece <= enough) break;
+  }
+}
 
 // clear_header: zero the workspace's control header on r.stream right before
 // the launch, after every host-side check has passed (a refused call leaves
@@ -516,7 +537,7 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
       // 7 sequences, group 2, head_dim 64, window 97: 25.7 in one, 18.0 in two.
       const int64_t units = (std::min<int64_t>(static_cast<int64_t>(r.max_blocks_per_seq) * r.block_size,
                                                static_cast<int64_t>(a.window) + a.num_sinks) + 15) / 16 + 1;
-      const int64_t pieces = std::min<int64_t>(L.pmax - 1, units);
+      const int64_t pieces = std::min<int64_t>(std::max<int64_t>(L.pmax - 1, inst.sinks.warps), units);
       while (a.group % 2 == 0 && static_cast<int64_t>(r.num_seqs) * a.num_kv_heads * pieces < 8LL * dinfo.sms) {
         a.group /= 2;
         a.num_kv_heads *= 2;
@@ -551,14 +572,9 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
       const int64_t need = (units_max * a.num_kv_heads + W - 1) / W;
       const int64_t at_least = (a.num_kv_heads + W - 1) / W;
       int64_t ctas = std::max(at_least, std::min<int64_t>(need, static_cast<int64_t>(dinfo.sms) * occ));
-      if (sinks) {
-        const int64_t wave = static_cast<int64_t>(dinfo.sms) * occ, seq_lists = static_cast<int64_t>(r.num_seqs) * a.num_kv_heads;
-        if (r.dtype == PA_BF16 && most_units(r, a.window, a.num_sinks) <= kWholeUnits16 && seq_lists <= wave * W)
-          a.seq_cut = 1;
-        else if (a.max_pieces <= kAlignedPieces && seq_lists * a.max_pieces <= wave * W)
-          a.seq_cut = a.max_pieces;
-        if (a.seq_cut > 0) ctas = (seq_lists * a.seq_cut + W - 1) / W;
-      }
+      if (sinks)
+        cut_sequences(r, a.num_kv_heads, most_units(r, a.window, a.num_sinks), W, static_cast<int64_t>(dinfo.sms) * occ,
+                      r.dtype == PA_F32 ? 1 : 2, &a, &ctas);
       grid = dim3(static_cast<unsigned>(ctas));
     } else {
       // Partition tickets (paged_decode_kernel, persistent mode).
@@ -612,7 +628,7 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
     err = cudaLaunchKernel(kernel, grid, dim3(threads), args, smem, r.stream);
   }
   if (err != cudaSuccess) return fail(PA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(err));
-  if (split && a.seq_cut != 1) {
+  if (split && a.seq_cut == 0) {
     st = launch_merge(inst.merge, r, a);
     if (st != PA_OK) return st;
   }
@@ -712,18 +728,7 @@ pa_status_t run_decode_q4(const DecodeReq& r, int window, int num_sinks, int par
   const int64_t W = inst.warps, lists = static_cast<int64_t>(r.num_kv_heads) * q_tiles;
   const int64_t need = (units_max * lists + W - 1) / W, at_least = (lists + W - 1) / W;
   int64_t ctas = std::max(at_least, std::min<int64_t>(need, static_cast<int64_t>(dinfo.sms) * occ));
-  const int64_t wave = static_cast<int64_t>(dinfo.sms) * occ, seq_lists = static_cast<int64_t>(r.num_seqs) * lists;
-  // As many pieces as a wave holds, but no more than make one step (4 units) each.
-  const int64_t most = most_units(r, window, num_sinks);
-  for (int64_t k = 1; k <= W; ++k) {
-    const int64_t each = W % k == 0 ? (seq_lists + W / k - 1) / (W / k) : wave + 1;
-    if (each > wave) continue;
-    if ((most + k - 1) / k <= kPieceUnits) {
-      a.seq_cut = static_cast<int>(k);
-      ctas = each;
-    }
-    if ((most + k - 1) / k <= 4) break;
-  }
+  cut_sequences(r, lists, most_units(r, window, num_sinks), W, static_cast<int64_t>(dinfo.sms) * occ, 4, &a, &ctas);
   const void *kp = r.k_pool, *vp = r.v_pool;
   void* args[] = {&kp, &vp, &q_tiles, &a};
   const cudaError_t err = cudaLaunchKernel(inst.kernel, dim3(static_cast<unsigned>(ctas)), dim3(inst.threads), args,

@@ -7,7 +7,7 @@
 // (every warp of a persistent grid an equal run of a KV head's list of 16-token
 // units, pieces merged by lse_merge_kernel), over lists that hold the sinks'
 // units and then the window's, so that no other block is read; short windows
-// and small tables are cut sequence by sequence (SinksArgs::seq_cut).
+// and small batches are cut sequence by sequence (SinksArgs::seq_cut).
 // Bound: 8 sequences of 100,000 to 131,072 tokens, window 4096 + 4, 64 heads
 // over 8 in bf16: 30.1 us (floor 20.6): 14 units a warp behind the launch, the
 // lists and the first loads, then the merge.
@@ -27,11 +27,9 @@ struct SinksArgs : DecodeArgs {
   // into several lists of fewer query heads (num_kv_heads and group are then
   // those of the lists), each reading the head's K and V.
   int head_tiles;
-  // Non-zero: each sequence's units are cut into so many equal pieces, and warp
-  // number w takes piece w / lists % cut of sequence w / lists / cut of list w %
-  // lists (a grid of as many warps). 1: whole sequences, and no merge follows.
-  // The 4-bit kernel's pieces are neighbouring warps of one CTA, a divisor of
-  // its consumers, and are merged there.
+  // Non-zero: each sequence's units are cut into so many equal pieces, for as
+  // many neighbouring warps of one CTA (a divisor of its consumers), which merge
+  // them there; no merge kernel follows.
   int seq_cut;
 };
 
@@ -158,23 +156,30 @@ __global__ void __launch_bounds__(Cfg::kThreads)
   const UnitLists lists = build_unit_lists<W>(a, BS, prefix, first_unit);
   const int U = lists.total;
   const int umax = lists.longest;
-  const int wg = static_cast<int>(blockIdx.x) * W + warp;
-  const int groups = static_cast<int>(gridDim.x) * W / Hkv;
-  const int h = wg % Hkv;   // this warp's KV head
-  const int gi = wg / Hkv;  // its group
-  const int kv_heads = Hkv / a.head_tiles, kv_head = h / a.head_tiles;  // of the pools
-  int C = max((U + groups - 1) / groups, (umax + a.max_pieces - 2) / (a.max_pieces - 1));
-  int64_t g_begin = static_cast<int64_t>(gi) * C, g_end = g_begin + C;
+  int h, gi = 0, g0, g1, C;  // this warp's list, its group, its units, and how the list is cut
+  int seq = 0, piece = 0;    // with seq_cut: its sequence and piece
   if (a.seq_cut > 0) {
-    const int seq = min(gi / a.seq_cut, B - 1), units = prefix[seq + 1] - prefix[seq];
-    C = (units + a.seq_cut - 1) / a.seq_cut;
-    g_begin = prefix[seq] + static_cast<int64_t>(gi % a.seq_cut) * C;
-    g_end = gi < B * a.seq_cut ? min(g_begin + C, static_cast<int64_t>(prefix[seq + 1])) : g_begin;
+    const int item = static_cast<int>(blockIdx.x) * (W / a.seq_cut) + warp / a.seq_cut;
+    h = item % Hkv;
+    seq = item / Hkv;
+    piece = warp % a.seq_cut;
+    const int first = prefix[min(seq, B)], end = prefix[min(seq + 1, B)];
+    C = (end - first + a.seq_cut - 1) / a.seq_cut;
+    g0 = min(first + piece * C, end);
+    g1 = min(g0 + C, end);
+  } else {
+    const int wg = static_cast<int>(blockIdx.x) * W + warp;
+    const int groups = static_cast<int>(gridDim.x) * W / Hkv;
+    h = wg % Hkv;
+    gi = wg / Hkv;
+    C = max((U + groups - 1) / groups, (umax + a.max_pieces - 2) / (a.max_pieces - 1));
+    const int64_t g_begin = static_cast<int64_t>(gi) * C;
+    g0 = static_cast<int>(g_begin < U ? g_begin : U);
+    g1 = gi < groups ? static_cast<int>(g_begin + C < U ? g_begin + C : U) : g0;
   }
-  const int g0 = static_cast<int>(g_begin < U ? g_begin : U);
-  const int g1 = static_cast<int>(g_end < U ? g_end : U);
-  const int nj = gi < groups ? g1 - g0 : 0;
-  if (nj <= 0) return;
+  const int kv_heads = Hkv / a.head_tiles, kv_head = h / a.head_tiles;  // of the pools
+  const int nj = g1 - g0;
+  if (nj <= 0 && a.seq_cut <= 1) return;
 
   // Sequence of unit g of a KV head's list (last s with prefix[s] <= g) and
   // the unit's index within the sequence's units.
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(Cfg::kThreads)
   // ---- consume the warp's units, segment by segment ---------------------------------
   WarpT st;
   int s = 0, un = 0;
-  locate(g0, s, un);
+  if (nj > 0) locate(g0, s, un);
   int us = prefix[s + 1] - prefix[s];
   int seg_start = g0 - un;  // index of the segment's first unit in h's list
   int ctx = 0, ftok = 0, ub = 0, ns = 0;  // ns: sink units at the segment's head
@@ -271,15 +276,15 @@ __global__ void __launch_bounds__(Cfg::kThreads)
     } else {
       st.begin(q_group, a.scale_log2, lane);
     }
-    if (un == 0) {  // this warp holds the segment's first piece: record the count
-      const int pieces = a.seq_cut > 0 ? (us + C - 1) / C : (seg_start + us - 1) / C - seg_start / C + 1;
+    if (un == 0 && a.seq_cut == 0) {  // this warp holds the segment's first piece: record the count
+      const int pieces = (seg_start + us - 1) / C - seg_start / C + 1;
       if (lane == 0) a.seg_pieces[static_cast<int64_t>(s) * Hkv + h] = pieces;
     }
   };
   // Writes the segment out: final rows when this warp covered all of it, else
   // the partial slot of this warp's piece.
   auto end_segment = [&](bool reached_end) {
-    const int piece = a.seq_cut > 0 ? gi % a.seq_cut : gi - seg_start / C;
+    const int piece = gi - seg_start / C;
     const bool whole = reached_end && seg_start >= g0;
     const int64_t row0 = static_cast<int64_t>(s) * a.num_q_heads + static_cast<int64_t>(h) * G;
     if constexpr (Cfg::kMma) {
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(Cfg::kThreads)
     }
   };
 
-  begin_segment();
+  if (nj > 0) begin_segment();
   bool timed_out = false;
   int j = 0;
   for (; j < nj; ++j) {
@@ -342,8 +347,45 @@ __global__ void __launch_bounds__(Cfg::kThreads)
     // Give copies still in flight a bounded chance to land before leaving.
     for (int jj = j; jj < min(nj, j + NS); ++jj)
       mbar_wait_bounded(&my_bars[jj % NS], (jj / NS) & 1u, a.dev_err);
-  } else {
+  } else if (a.seq_cut <= 1) {
     end_segment(un == us);
+  }
+  if (a.seq_cut <= 1) return;
+
+  // ---- pieces of one sequence, merged in shared memory: a warp's state takes the
+  // place of its ring, whose last copies it has used ----------------------------------
+  constexpr int kRows = Cfg::kRowsMax;
+  static_assert(kRows * (D + 2) * 4 <= NS * Cfg::kStageBytes, "a warp's state fits its ring");
+  auto state = [&](int w) { return reinterpret_cast<float*>(ring + w * NS * Cfg::kStageBytes); };  // m, l, values
+  float* mine = state(warp);
+  if (nj <= 0) {
+    if (lane < kRows) mine[lane] = -INFINITY;
+  } else if constexpr (Cfg::kMma) {
+    st.publish(mine, mine + kRows, mine + 2 * kRows, G, lane);
+  } else {
+    st.publish(mine, mine + kRows, mine + 2 * kRows, lane);
+  }
+  __syncthreads();
+  if (seq >= B) return;
+  for (int r = piece; r < G; r += a.seq_cut) {
+    const int w0 = warp - piece;
+    float top = -INFINITY;
+    for (int p = 0; p < a.seq_cut; ++p) top = fmaxf(top, state(w0 + p)[r]);
+    float sum = 0.f, acc[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+    for (int p = 0; p < a.seq_cut; ++p) {
+      const float* from = state(w0 + p);
+      if (from[r] == -INFINITY) continue;  // (no token: its values may be anything)
+      const float wt = fast_exp2(from[r] - top);
+      sum = fmaf(from[kRows + r], wt, sum);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(from[2 * kRows + r * D + lane + 32 * i], wt, acc[i]);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    T* out = reinterpret_cast<T*>(a.out) + (static_cast<int64_t>(seq) * a.num_q_heads + static_cast<int64_t>(h) * G + r) * D;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) out[lane + 32 * i] = Elt<T>::from_f32(acc[i] * inv);
   }
 }
 
