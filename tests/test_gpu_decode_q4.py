@@ -297,3 +297,23 @@ def test_short_sequences_whole_and_cut(num, Hkv, window, sinks):
     rng = np.random.default_rng(num)
     lens = [127, 0][:num] + rng.integers(0, 128, max(0, num - 2)).tolist()
     check(*make(num, lens, 2 * Hkv, Hkv, 128, 16, slack=0), 16, window, sinks)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("top", [63, 100, 190, 380, 700])
+def test_every_number_of_pieces_in_a_cta(D, top):
+    """One sequence of `top` tokens sets how many warps share each sequence; the
+    others leave some of them without units. Nine query heads: two runs of heads."""
+    check(*make(D + top, [top, 1, 0, top // 2, 17], 18, 2, D, 16, slack=0), 16, partition_tokens=512)
+
+
+def test_pieces_in_a_cta_equal_equal_runs():
+    """The same sequences in a small batch (merged in the CTA) and in a batch that a
+    wave cannot hold (equal runs and the merge kernel)."""
+    q, k, v, tables, lens = make(23, [300, 1, 160] + [200] * 900, 4, 2, 64, 16, slack=0)
+    args = [torch.from_numpy(x).cuda() for x in (k, v, tables, lens)]
+    many = binding.decode_q4(q.cuda(), *args, 0.1)
+    few = binding.decode_q4(q[:3].cuda(), *args[:2], args[2][:3].contiguous(), args[3][:3], 0.1)
+    # both within the bound of check(); against each other twice that, here two bf16 steps
+    assert torch.all((many[:3].float() - few.float()).abs() <= 2.0 ** -6 * few.float().abs() + 2e-2)
+    check(q[:3], k, v, tables[:3], lens[:3], 16)
