@@ -39,9 +39,9 @@
 //   its two layouts by movmatrix. f16 needs the weights' range bounded: see
 //   Q4Warp::expo. In exchange O accumulates in place, where a mask-or'ed bf16
 //   code (128 + c) would leave a cancellation of 128 to a few.
-// * Steps of 64 tokens share one running maximum; the accumulators are rescaled
-//   only when it (or expo) moves. Steps that are not whole go unit by unit
-//   through the masked build.
+// * A step (64 tokens at head_dim 128, 128 at 64, 48 at 256) shares one running
+//   maximum; the accumulators are rescaled only when it (or expo) moves. Steps
+//   that are not whole go unit by unit through the masked build.
 // Rounding: q to 16 bits of its head's range (at most 2^-15 of the largest),
 // p s to f16 (2^-11), the output to bf16; sums, logits, minima in fp32 or exact.
 // Bound: 8 x 131072 tokens (64 heads over 8, head_dim 128) take 250 us, 1.21 GB
@@ -58,8 +58,9 @@
 
 namespace pagedkv {
 
-// W consumer warps and four producer warps; a step takes up to US units; each consumer's ring has NS slots of US sub-tiles, filled
-// in the order K, V, K, V, ... of its steps.
+// W consumer warps and four producer warps; a step takes up to US units (a
+// producer has eight lanes per consumer); each consumer's ring has NS slots of US
+// sub-tiles, filled in the order K, V, K, V, ... of its steps.
 template <int BS_, int D_, int W_, int US_, int NS_>
 struct Q4Cfg {
   static constexpr int BS = BS_, D = D_, W = W_, US = US_, NS = NS_;
@@ -75,7 +76,7 @@ struct Q4Cfg {
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
   static constexpr int kProducerRegs = W == 12 ? 32 : 40;
   static constexpr int kConsumerRegs = (kLaunchRegs * (W + 4) - kProducerRegs * 4) / W / 8 * 8;
-  static_assert(W % 4 == 0 && W <= 12 && US <= 4 && NS >= 2 && NS <= 8, "whole warpgroups; ring layout");
+  static_assert(W % 4 == 0 && W <= 12 && US <= 8 && NS >= 2 && NS <= 8, "whole warpgroups; ring layout");
   static_assert(kConsumerRegs * W + kProducerRegs * 4 <= kLaunchRegs * (W + 4), "registers of the split");
   static_assert(kRingBytes % 16 == 0 && kFixedSmem + (2 * 4096 + 1) * 4 <= 226 * 1024, "shared memory budget exceeded");
 };
