@@ -317,3 +317,12 @@ def test_pieces_in_a_cta_equal_equal_runs():
     # both within the bound of check(); against each other twice that, here two bf16 steps
     assert torch.all((many[:3].float() - few.float()).abs() <= 2.0 ** -6 * few.float().abs() + 2e-2)
     check(q[:3], k, v, tables[:3], lens[:3], 16)
+
+
+@pytest.mark.parametrize("D,num,window,sinks", [(64, 420, 0, 0), (64, 420, 131, 5), (256, 140, 0, 0), (256, 140, 50, 3)])
+def test_whole_steps_and_their_remainders(D, num, window, sinks):
+    """Runs of many steps for every warp: sequences around whole steps (eight units
+    at head_dim 64, three at 256) and such that end inside one."""
+    rng = np.random.default_rng(D + window)
+    lens = [127, 128, 129, 255, 256, 257, 47, 48, 49, 95, 96, 97] + rng.integers(100, 330, num - 12).tolist()
+    check(*make(D, lens, 16, 8, D, 16 if window else 32, slack=0), 16 if window else 32, window, sinks)
