@@ -8,6 +8,7 @@ shared library is missing, the first call raises ``RuntimeError``.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -213,6 +214,17 @@ def _stream_ptr(stream) -> int:
     return stream.cuda_stream
 
 
+def _allocating_for(stream):
+    """What a call allocates belongs to the stream it runs on: memory of another
+    stream's could still be in use there, or be given away while the call runs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
 def _require_cuda(*tensors):
     for t in tensors:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -266,8 +278,9 @@ class SplitWorkspace:
         torch = _torch()
         self.nbytes = decode_split_workspace_size(num_seqs, num_q_heads, head_dim, block_size,
                                                   max_blocks_per_seq, partition_tokens)
-        self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8,
-                                  device=device or torch.device("cuda"))
+        with _allocating_for(stream):
+            self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8,
+                                      device=device or torch.device("cuda"))
         base = self.buffer.data_ptr()
         self.ptr = (base + 255) & ~255
         _check(library().pa_decode_split_workspace_init(self.ptr, self.nbytes, _stream_ptr(stream)))
@@ -495,7 +508,8 @@ def decode_split_sinks(q, k_pool, v_pool, block_tables, context_lens, scale: flo
     first ``sinks``. A given workspace sets partition_tokens."""
     torch = _torch()
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating_for(stream):
+            out = torch.empty_like(q)
     B, Hq, D, NB, Hkv, BS, MBS = _decode_common(q, k_pool, v_pool, block_tables, context_lens, out)
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
@@ -570,8 +584,9 @@ def kv_gather_q4(k_pool, v_pool, slot_mapping, head_dim: int, dtype=None, out=No
         raise _bad("slot_mapping must be int64 [tokens]")
     T = slot_mapping.size(0)
     if out is None:
-        k_out = torch.empty((T, Hkv, head_dim), dtype=dtype or torch.bfloat16, device=k_pool.device)
-        v_out = torch.empty_like(k_out)
+        with _allocating_for(stream):
+            k_out = torch.empty((T, Hkv, head_dim), dtype=dtype or torch.bfloat16, device=k_pool.device)
+            v_out = torch.empty_like(k_out)
     else:
         k_out, v_out = out
         _on_device(k_pool, k_out, v_out)
@@ -592,7 +607,8 @@ def decode_q4(q, k_pool, v_pool, block_tables, context_lens, scale: float, windo
     whole context. A given workspace (SplitWorkspace) sets partition_tokens."""
     torch = _torch()
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating_for(stream):
+            out = torch.empty_like(q)
     shape = B, Hq, D = q.shape
     NB, Hkv, BS = _q4_pool_shape(k_pool, v_pool, D)
     _on_device(q, k_pool, v_pool, block_tables, context_lens, out)
@@ -662,7 +678,8 @@ def rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_pool, v_po
             raise _bad("q must have the tokens, head_dim, type and device of k_new")
         q_stride = _token_rows(q, Hq, D, "q")
         if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            with _allocating_for(stream):
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         elif (q_out.shape != q.shape or q_out.dtype != dtype or q_out.get_device() != dev
               or not q_out.is_contiguous()):
             raise _bad("q_out must be contiguous, of q's shape and type")
@@ -706,7 +723,8 @@ def extend_tables(block_tables, context_lens, new_lens, free_queue, queue_state,
     torch = _torch()
     B, MBS = block_tables.shape
     if out is None:
-        out = StepTables.empty(B, max_tokens, block_tables.device)
+        with _allocating_for(stream):
+            out = StepTables.empty(B, max_tokens, block_tables.device)
     lens, start, pos, slots, state = (out.context_lens, out.query_start, out.positions,
                                       out.slot_mapping, out.queue_state)
     _on_device(block_tables, context_lens, new_lens, free_queue, queue_state, lens, start, pos,

@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -639,17 +640,18 @@ pa_status_t run_decode(const DecodeReq& r, bool split, int partition_tokens, voi
 // with; fewer than it counts on would leave them waiting, so that is looked at
 // once per kernel.
 pa_status_t check_launch_regs(const void* kernel, int regs) {
-  static std::mutex mu;
-  static std::vector<const void*> done;
-  std::lock_guard<std::mutex> lock(mu);
-  for (const void* k : done)
-    if (k == kernel) return PA_OK;
+  static std::atomic<const void*> done[8];  // six kernels: three head sizes, two block sizes
+  for (auto& k : done)
+    if (k.load(std::memory_order_relaxed) == kernel) return PA_OK;
   cudaFuncAttributes at{};
   const cudaError_t err = cudaFuncGetAttributes(&at, kernel);
   if (err != cudaSuccess) return fail(PA_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(err));
   if (at.numRegs != regs)
     return fail(PA_ERR_UNSUPPORTED, "the 4-bit kernel was built with %d registers a thread, not %d", at.numRegs, regs);
-  done.push_back(kernel);
+  for (auto& k : done) {
+    const void* none = nullptr;
+    if (k.compare_exchange_strong(none, kernel, std::memory_order_relaxed)) break;
+  }
   return PA_OK;
 }
 

@@ -229,3 +229,37 @@ def test_two_streams_at_once():
         assert all(torch.equal(o, outs[i % 2]) for i, o in enumerate(outs))
         res.append(outs[:2])
     assert all(torch.equal(x, y) for x, y in zip(*res))
+
+
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """With `stream`, outputs and the workspace come from that stream's memory: the
+    current stream's next tensors never take it while the call may still run."""
+    loop = Loop(True, 13)
+    q, st = loop.step([30, 5, 16, 31, 64])
+    k = torch.zeros(64, HKV, D, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(64, dtype=torch.int32, device="cuda")
+    slots = torch.full((64,), -1, dtype=torch.int64, device="cuda")
+    pools = [torch.zeros(NB, HKV, BS, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    q1 = q[:B].contiguous()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    calls = [
+        lambda: binding.SplitWorkspace(B, HQ, D, BS, MBS, 32, stream=side).buffer,
+        lambda: binding.decode_q4(q1, loop.k, loop.v, loop.tables, loop.lens, 0.1, stream=side),
+        lambda: binding.decode_split_sinks(q1, *pools, loop.tables, loop.lens, 0.1, 50, 4, stream=side),
+        lambda: binding.kv_gather_q4(loop.k, loop.v, slots, D, stream=side)[0],
+        lambda: binding.rope_append(k, k, k, pos, loop.inv, slots, *pools, stream=side),
+        lambda: binding.extend_tables(loop.tables, loop.lens, zero, loop.queue, loop.state, BS, 64,
+                                      stream=side).slot_mapping,
+    ]
+    for call in calls:
+        t = call()
+        at, n = t.data_ptr(), t.untyped_storage().nbytes()
+        torch.cuda.synchronize()
+        del t
+        here = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        assert at not in [x.data_ptr() for x in here]
+        with torch.cuda.stream(side):
+            there = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        assert at in [x.data_ptr() for x in there]
