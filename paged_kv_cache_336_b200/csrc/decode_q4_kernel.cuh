@@ -815,7 +815,7 @@ __device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, cons
     }
     if (g == 0) {
       mine[8 * D + 2 * t + e] = st.m[e];
-      mine[8 * D + 8 + 2 * t + e] = some ? st.l[e] : 0.f;
+      mine[8 * D + 8 + 2 * t + e] = some ? st.l[e] : -1.f;  // (a sum is at least 0, or NaN)
     }
   }
   named_bar_sync(1, 32 * W);
@@ -824,14 +824,16 @@ __device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, cons
   for (int hd = run.piece; hd < heads; hd += a.seq_cut) {
     float top = -INFINITY;
     for (int p = 0; p < a.seq_cut; ++p) top = fmaxf(top, state(w0 + p)[8 * D + hd]);
+    // A maximum of -inf does not tell a piece without a token from one whose logits
+    // are all NaN (which fmaxf passes over): the latter weighs 0, and 0 * NaN is NaN.
+    if (top == -INFINITY) top = 0.f;
     float sum = 0.f, acc[D / 32];
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
     for (int p = 0; p < a.seq_cut; ++p) {
       const float* from = state(w0 + p);
-      const float pm = from[8 * D + hd];
-      if (pm == -INFINITY) continue;  // (no token: nothing was written)
-      const float wt = fast_exp2(pm - top);
+      if (from[8 * D + 8 + hd] < 0.f) continue;  // no unit: its values may be anything
+      const float wt = fast_exp2(from[8 * D + hd] - top);
       sum = fmaf(from[8 * D + 8 + hd], wt, sum);
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(from[hd * D + 2 * lane + 64 * (j / 2) + (j & 1)], wt, acc[j]);
