@@ -359,7 +359,10 @@ __global__ void __launch_bounds__(Cfg::kThreads)
   auto state = [&](int w) { return reinterpret_cast<float*>(ring + w * NS * Cfg::kStageBytes); };  // m, l, values
   float* mine = state(warp);
   if (nj <= 0) {
-    if (lane < kRows) mine[lane] = -INFINITY;
+    if (lane < kRows) {
+      mine[lane] = -INFINITY;
+      mine[kRows + lane] = -1.f;  // (a sum is at least 0, or NaN)
+    }
   } else if constexpr (Cfg::kMma) {
     st.publish(mine, mine + kRows, mine + 2 * kRows, G, lane);
   } else {
@@ -371,12 +374,15 @@ __global__ void __launch_bounds__(Cfg::kThreads)
     const int w0 = warp - piece;
     float top = -INFINITY;
     for (int p = 0; p < a.seq_cut; ++p) top = fmaxf(top, state(w0 + p)[r]);
+    // A maximum of -inf does not tell a piece without a token from one whose logits
+    // are all NaN (which fmaxf passes over): the latter weighs 0, and 0 * NaN is NaN.
+    if (top == -INFINITY) top = 0.f;
     float sum = 0.f, acc[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
     for (int p = 0; p < a.seq_cut; ++p) {
       const float* from = state(w0 + p);
-      if (from[r] == -INFINITY) continue;  // (no token: its values may be anything)
+      if (from[kRows + r] < 0.f) continue;  // no unit: its values may be anything
       const float wt = fast_exp2(from[r] - top);
       sum = fmaf(from[kRows + r], wt, sum);
 #pragma unroll

@@ -1,6 +1,6 @@
 """NaN and infinities among queries and keys, in every way in which the 4-bit
-decode cuts a batch: pieces of a sequence merged in a CTA, one warp a sequence,
-equal runs with the merge kernel.
+decode and the windowed decode with sinks cut a batch: pieces of a sequence
+merged in a CTA, one warp a sequence, equal runs with the merge kernel.
 
 By the definition, a head's output is NaN as soon as one visible logit is NaN
 (whatever the others are), and every other row is what it is without the NaN,
@@ -91,3 +91,28 @@ def test_4bit_decode(D, Hq, Hkv, way, window, sinks):
             assert set(tokens) & set(visible)
             k2[torch.from_numpy(slots_of(own, s, tokens)).cuda(), 0, D - 1] = what
         expect(call(q2, k2), clean, Hq, Hq // Hkv, bad_q)
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("dtype,D,Hq,Hkv", [(torch.float32, 64, 4, 2), (torch.float32, 128, 8, 1),
+                                            (torch.bfloat16, 64, 8, 2), (torch.bfloat16, 128, 16, 1),
+                                            (torch.bfloat16, 256, 2, 1)])
+@pytest.mark.parametrize("window,sinks", [(100, 4), (10_000, 0)])
+def test_windows_with_sinks(dtype, D, Hq, Hkv, way, window, sinks):
+    # the rings leave room for 8 (head_dim 128) to 24 (64) warps a multiprocessor
+    num = num_seqs(way, 24 if way == "runs" else 8, Hkv)
+    tables, lens, own = batch(num)
+    g = torch.Generator(device="cuda").manual_seed(D + Hq)
+    k, v = (torch.randn(9 * BLOCKS, Hkv, BS, D, device="cuda", generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(num, Hq, D, device="cuda", generator=g).to(dtype)
+
+    def call(q, k):
+        return binding.decode_split_sinks(q, k, v, tables, lens, 0.1, window, sinks, partition_tokens=PARTITION[way])
+
+    clean = call(q, k)
+    q2, k2 = q.clone(), k.clone()
+    q2[0, Hq - 1, D // 2 + 1] = float("nan")
+    for s, tokens in BAD_KEYS.items():
+        slot = torch.from_numpy(slots_of(own, s, tokens)).cuda()
+        k2[slot // BS, 0, slot % BS, D - 1] = float("nan")
+    expect(call(q2, k2), clean, Hq, Hq // Hkv, Hq - 1)
