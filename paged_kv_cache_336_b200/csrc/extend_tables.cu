@@ -347,7 +347,10 @@ extern "C" pa_status_t pa_extend_tables(int32_t* block_tables, const int32_t* co
   const int64_t work = std::max<int64_t>((static_cast<int64_t>(max_tokens) + 3) / 4, num_seqs);
   const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((work + kExtThreads - 1) / kExtThreads, 2 * 148)));
   const size_t smem = (static_cast<size_t>(num_seqs) * 4 + 2) * sizeof(int);
-  if (smem > 48 * 1024) {
+  // Without the opt-in dynamic and static shared memory (some 200 bytes here)
+  // together may take 48 KB.
+  constexpr size_t kStaticRoom = 1024;
+  if (smem + kStaticRoom > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(extend_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>((kExtMaxSeqs * 4 + 2) * sizeof(int)));
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "extend_tables: %s", cudaGetErrorString(e));
