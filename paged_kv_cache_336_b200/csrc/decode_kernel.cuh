@@ -201,9 +201,7 @@ struct SimtWarp {
   }
 
   // Tokens nfirst <= t < nvalid of the unit take part (nfirst > 0 only in the
-  // first unit of a sliding window). kGuard: a head whose logits so far are all
-  // -inf keeps its state (2^(-inf - -inf) would make it NaN).
-  template <bool kGuard = false>
+  // first unit of a sliding window).
   __device__ __forceinline__ void block(const uint8_t* kt, uint8_t* vt, int nfirst, int nvalid,
                                         int lane) {
     const int byte_off = lane * VEC * Geo::kElt;
@@ -224,9 +222,8 @@ struct SimtWarp {
       transpose_reduce<BS>(v, lane);
       const float s = (my_token >= nfirst && my_token < nvalid) ? v[0] : -INFINITY;
       const float m_new = fmaxf(m[h], warp_max(s));
-      const bool none = kGuard && m_new == -INFINITY;
-      const float alpha = none ? 1.f : fast_exp2(m[h] - m_new);
-      const float p = fast_exp2(none ? s : s - m_new);
+      const float alpha = fast_exp2(m[h] - m_new);
+      const float p = fast_exp2(s - m_new);
       l[h] = l[h] * alpha + (counts ? p : 0.f);
       m[h] = m_new;
 #pragma unroll
@@ -333,12 +330,11 @@ struct MmaWarp {
     scale_log2 = scale;
   }
 
-  template <bool kGuard = false>
   __device__ __forceinline__ void block(const uint8_t* kt, uint8_t* vt, int nfirst, int nvalid,
                                         int lane) {
     const uint8_t* kts[1] = {kt};
     uint8_t* vts[1] = {vt};
-    block_units<1, false, kGuard>(kts, vts, nfirst, nvalid, lane);
+    block_units<1>(kts, vts, nfirst, nvalid, lane);
   }
 
   // U consecutive 16-token units (tiles kts[u], vts[u]) in one online-softmax
@@ -348,10 +344,9 @@ struct MmaWarp {
   // part; the caller guarantees at least one.
   //
   // kRowLimits (causal prefill): in addition, token t counts for fragment row
-  // g only while t <= lim0 and for row g+8 only while t <= lim1. kGuard: a row
-  // whose logits so far are all -inf (no token in the span) keeps its state
-  // (guards against -inf - -inf).
-  template <int U, bool kRowLimits = false, bool kGuard = kRowLimits>
+  // g only while t <= lim0 and for row g+8 only while t <= lim1; a row with
+  // no token in the span keeps its state (guards against -inf - -inf).
+  template <int U, bool kRowLimits = false>
   __device__ __forceinline__ void block_units(const uint8_t* const (&kts)[U], uint8_t* const (&vts)[U],
                                               int nfirst, int nvalid, int lane, int lim0 = 0,
                                               int lim1 = 0) {
@@ -400,7 +395,7 @@ struct MmaWarp {
     float mn0 = fmaxf(m[0], mx0);
     float mn1 = fmaxf(m[1], mx1);
     float a0, a1;
-    if constexpr (kGuard) {
+    if constexpr (kRowLimits) {
       // A row with nothing valid so far has mn == -inf: keep alpha 1, p 0.
       a0 = (mn0 == -INFINITY) ? 1.f : fast_exp2(m[0] - mn0);
       a1 = (mn1 == -INFINITY) ? 1.f : fast_exp2(m[1] - mn1);
@@ -410,7 +405,7 @@ struct MmaWarp {
     }
     m[0] = mn0;
     m[1] = mn1;
-    if constexpr (kGuard) {
+    if constexpr (kRowLimits) {
       if (mn0 == -INFINITY) mn0 = 0.f;   // every s of the row is -inf: 2^(-inf) = 0
       if (mn1 == -INFINITY) mn1 = 0.f;
     }

@@ -3,9 +3,8 @@
 // lists that the 4-bit decode kernel shares.
 //
 // What is computed: softmax(scale * K_s q) V_s over tokens t < ctx with
-// t >= ctx - window or t < num_sinks; a logit of -inf weighs nothing, and a row of
-// nothing but such logits is zeros, as one without a token.
-// How: paged_decode_stream_kernel's cut (every warp of a persistent grid an equal run of a KV head's list of 16-token
+// t >= ctx - window or t < num_sinks. How: paged_decode_stream_kernel's cut
+// (every warp of a persistent grid an equal run of a KV head's list of 16-token
 // units, pieces merged by lse_merge_kernel), over lists that hold the sinks'
 // units and then the window's, so that no other block is read; short windows
 // and small batches are cut sequence by sequence (SinksArgs::seq_cut).
@@ -18,9 +17,9 @@
 
 namespace pagedkv {
 
-// Running maximum of a piece in which no token weighs (every block id bad, logits
-// of -inf or NaN), for the merge: the lowest finite value.
-constexpr float kNoTokens = -3.402823466e38f;
+// Running maximum of a piece in which no token was found (every block id bad),
+// for the merge: finite, below any logit.
+constexpr float kNoTokens = -1e30f;
 
 struct SinksArgs : DecodeArgs {
   int num_sinks;  // first tokens that stay visible beside the window
@@ -337,7 +336,7 @@ __global__ void __launch_bounds__(Cfg::kThreads)
       const int nfirst = sink ? 0 : ftok - u0;          // > 0 only inside the window's first unit
       if (nfirst < nvalid) {
         uint8_t* kt = my_ring + stage * Cfg::kStageBytes;
-        st.template block<true>(kt, kt + Geo::kTileBytes, nfirst, nvalid, lane);
+        st.block(kt, kt + Geo::kTileBytes, nfirst, nvalid, lane);
       }
     }
     __syncwarp();
