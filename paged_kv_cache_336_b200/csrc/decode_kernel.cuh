@@ -833,18 +833,17 @@ __global__ void __launch_bounds__(Cfg::kThreads)
 #pragma unroll
       for (int w = 0; w < W; ++w) M = fmaxf(M, sm_m[w * Cfg::kRowsMax + h]);
       float L = 0.f, A = 0.f;
-      // M is -inf without a token, and also where every logit is NaN (fmaxf passes
-      // over it): the sums then are 0 or NaN, and a weight of 0 keeps either.
-      const float top = M == -INFINITY ? 0.f : M;
+      if (M != -INFINITY) {
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float e = fast_exp2(sm_m[w * Cfg::kRowsMax + h] - top);
-        L = fmaf(sm_l[w * Cfg::kRowsMax + h], e, L);
-        A = fmaf(sm_acc[(w * Cfg::kRowsMax + h) * D + d], e, A);
+        for (int w = 0; w < W; ++w) {
+          const float e = fast_exp2(sm_m[w * Cfg::kRowsMax + h] - M);
+          L = fmaf(sm_l[w * Cfg::kRowsMax + h], e, L);
+          A = fmaf(sm_acc[(w * Cfg::kRowsMax + h) * D + d], e, A);
+        }
       }
       const int64_t row = row0 + h;
       if (final_out) {
-        reinterpret_cast<T*>(a.out)[row * D + d] = Elt<T>::from_f32(L == 0.f ? 0.f : A / L);
+        reinterpret_cast<T*>(a.out)[row * D + d] = Elt<T>::from_f32(L > 0.f ? A / L : 0.f);
       } else {
         const int64_t pr = row * a.max_partitions + part_base + p;
         a.part_acc[pr * D + d] = A;
