@@ -1,4 +1,8 @@
-// Library-wide C-ABI helpers: version, status names, per-thread last error.
+// Library-wide helpers: version, status names, per-thread last error,
+// multiprocessors of the current device.
+#include <cuda_runtime_api.h>
+
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
@@ -22,6 +26,20 @@ pa_status_t fail(pa_status_t status, const char* fmt, ...) {
 pa_status_t ok() {
   g_last_error.clear();
   return PA_OK;
+}
+
+int sm_count() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 148;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (n <= 0) n = 148;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 }  // namespace pagedkv

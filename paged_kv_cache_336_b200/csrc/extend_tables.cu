@@ -345,7 +345,7 @@ extern "C" pa_status_t pa_extend_tables(int32_t* block_tables, const int32_t* co
   // tokens as well. At most two CTAs per SM: each repeats the prefix sums
   // (four take 12.8 us instead of 11.7 for 512 sequences with 465,000 tokens).
   const int64_t work = std::max<int64_t>((static_cast<int64_t>(max_tokens) + 3) / 4, num_seqs);
-  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((work + kExtThreads - 1) / kExtThreads, 2 * 148)));
+  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((work + kExtThreads - 1) / kExtThreads, 2 * sm_count())));
   const size_t smem = (static_cast<size_t>(num_seqs) * 4 + 2) * sizeof(int);
   // Without the opt-in dynamic and static shared memory (some 200 bytes here)
   // together may take 48 KB.

@@ -165,13 +165,6 @@ pa_status_t launch_swap(const void* src_k, const void* src_v, void* dst_k, void*
   return ok();
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 148;
-}
-
 }  // namespace
 bool validate_copy_pairs() {
   static const bool enabled = [] {

@@ -15,6 +15,9 @@ pa_status_t fail(pa_status_t status, const char* fmt, ...);
 // Clears the calling thread's last error; returns PA_OK.
 pa_status_t ok();
 
+// Multiprocessors of the current device, asked for once per device.
+int sm_count();
+
 }  // namespace pagedkv
 
 // NVTX ranges around the C-ABI calls that enqueue GPU work, so that a

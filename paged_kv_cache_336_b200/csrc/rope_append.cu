@@ -31,7 +31,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -510,21 +509,6 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Multiprocessors of the current device, asked for once per device.
-int sm_count() {
-  constexpr int kDevices = 64;
-  static std::atomic<int> known[kDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 148;
-  int n = known[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (n <= 0) n = 148;
-    known[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
 
 template <typename T, int D, bool kInterleaved, bool kQ4>
 void launch_rope(RopeArgs p, cudaStream_t stream) {
