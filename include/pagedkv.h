@@ -277,7 +277,9 @@ pa_status_t pa_decode_split_window(const void* q, const void* k_pool, const void
  * stay visible beside the window, so the query attends to tokens t < ctx with
  * t >= ctx - window or t < num_sinks (window >= 1, num_sinks >= 0). Blocks
  * that hold neither a sink nor a token of the window are never read and their
- * table entries may be -1. fp32 and bf16, the shapes of pa_decode_split. Large
+ * table entries may be -1. A logit of -inf weighs nothing; a query head without
+ * a visible token, or with such logits only, gets zeros. A visible NaN makes its
+ * heads NaN. fp32 and bf16, the shapes of pa_decode_split. Large
  * batches are cut as pa_decode_split cuts long tables, small ones sequence by
  * sequence. Same workspace and contract as pa_decode_split.
  * ------------------------------------------------------------------------- */

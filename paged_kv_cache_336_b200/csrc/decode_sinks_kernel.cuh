@@ -3,8 +3,9 @@
 // lists that the 4-bit decode kernel shares.
 //
 // What is computed: softmax(scale * K_s q) V_s over tokens t < ctx with
-// t >= ctx - window or t < num_sinks. How: paged_decode_stream_kernel's cut
-// (every warp of a persistent grid an equal run of a KV head's list of 16-token
+// t >= ctx - window or t < num_sinks; a logit of -inf weighs nothing, and a row of
+// nothing but such logits is zeros, as one without a token.
+// How: paged_decode_stream_kernel's cut (every warp of a persistent grid an equal run of a KV head's list of 16-token
 // units, pieces merged by lse_merge_kernel), over lists that hold the sinks'
 // units and then the window's, so that no other block is read; short windows
 // and small batches are cut sequence by sequence (SinksArgs::seq_cut).
@@ -17,9 +18,10 @@
 
 namespace pagedkv {
 
-// Running maximum of a piece in which no token was found (every block id bad),
-// for the merge: finite, below any logit.
-constexpr float kNoTokens = -1e30f;
+// Running maximum before the first token, and of a piece without weight (every
+// block id bad, logits of -inf or NaN): the lowest finite value. From -inf the
+// first step would take 2^(-inf - -inf), a NaN, where its logits are -inf.
+constexpr float kNoTokens = -3.402823466e38f;
 
 struct SinksArgs : DecodeArgs {
   int num_sinks;  // first tokens that stay visible beside the window
@@ -276,6 +278,7 @@ __global__ void __launch_bounds__(Cfg::kThreads)
     } else {
       st.begin(q_group, a.scale_log2, lane);
     }
+    for (float& m : st.m) m = kNoTokens;
     if (un == 0 && a.seq_cut == 0) {  // this warp holds the segment's first piece: record the count
       const int pieces = (seg_start + us - 1) / C - seg_start / C + 1;
       if (lane == 0) a.seg_pieces[static_cast<int64_t>(s) * Hkv + h] = pieces;
@@ -293,8 +296,6 @@ __global__ void __launch_bounds__(Cfg::kThreads)
         T* o = reinterpret_cast<T*>(a.out) + row0 * D;
         st.store_final(o + g * D, o + (g + 8) * D, g < G, g + 8 < G, lane);
       } else {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) st.m[r] = st.m[r] == -INFINITY ? kNoTokens : st.m[r];
         const int64_t pr0 = g < G ? (row0 + g) * a.max_partitions + piece : -1;
         const int64_t pr1 = g + 8 < G ? (row0 + g + 8) * a.max_partitions + piece : -1;
         st.store_partials(a, pr0, pr1, lane);
@@ -303,8 +304,6 @@ __global__ void __launch_bounds__(Cfg::kThreads)
       if (whole) {
         st.store_final(reinterpret_cast<T*>(a.out) + row0 * D, lane);
       } else {
-#pragma unroll
-        for (int r = 0; r < WarpT::G; ++r) st.m[r] = st.m[r] == -INFINITY ? kNoTokens : st.m[r];
         st.store_partials(a, row0 * a.max_partitions + piece, a.max_partitions, lane);
       }
     }
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(Cfg::kThreads)
   float* mine = state(warp);
   if (nj <= 0) {
     if (lane < kRows) {
-      mine[lane] = -INFINITY;
+      mine[lane] = kNoTokens;
       mine[kRows + lane] = -1.f;  // (a sum is at least 0, or NaN)
     }
   } else if constexpr (Cfg::kMma) {
@@ -372,11 +371,10 @@ __global__ void __launch_bounds__(Cfg::kThreads)
   if (seq >= B) return;
   for (int r = piece; r < G; r += a.seq_cut) {
     const int w0 = warp - piece;
-    float top = -INFINITY;
+    // A piece whose logits are all NaN has the maximum of one without a token
+    // (fmaxf passes over NaN), but sums of NaN, which any weight keeps.
+    float top = kNoTokens;
     for (int p = 0; p < a.seq_cut; ++p) top = fmaxf(top, state(w0 + p)[r]);
-    // A maximum of -inf does not tell a piece without a token from one whose logits
-    // are all NaN (which fmaxf passes over): the latter weighs 0, and 0 * NaN is NaN.
-    if (top == -INFINITY) top = 0.f;
     float sum = 0.f, acc[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;

@@ -12,7 +12,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import attention_definition
 from paged_kv_cache_336_b200 import binding
+
+from gpu_util import BF16_MAX_ABS, F32_MAX_ABS, to_f64
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +119,34 @@ def test_windows_with_sinks(dtype, D, Hq, Hkv, way, window, sinks):
         slot = torch.from_numpy(slots_of(own, s, tokens)).cuda()
         k2[slot // BS, 0, slot % BS, D - 1] = float("nan")
     expect(call(q2, k2), clean, Hq, Hq // Hkv, Hq - 1)
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("dtype,D,Hq,Hkv", [(torch.float32, 64, 4, 2), (torch.bfloat16, 64, 8, 2),
+                                            (torch.bfloat16, 128, 16, 1)])
+@pytest.mark.parametrize("window,sinks", [(100, 4), (10_000, 0)])
+def test_logits_of_minus_infinity_weigh_nothing(dtype, D, Hq, Hkv, way, window, sinks):
+    """Keys that make every head's logit -inf, where BAD_KEYS has them: the softmax of
+    the others; nothing but such logits (sequence 2): zeros."""
+    num = num_seqs(way, 24 if way == "runs" else 8, Hkv)
+    tables, lens, own = batch(num)
+    g = torch.Generator(device="cuda").manual_seed(D + Hq)
+    k, v = (torch.randn(9 * BLOCKS, Hkv, BS, D, device="cuda", generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(num, Hq, D, device="cuda", generator=g).to(dtype)
+    q[..., D - 1] = q[..., D - 1].abs() + 0.5
+    for s, tokens in BAD_KEYS.items():
+        slot = torch.from_numpy(slots_of(own, s, tokens)).cuda()
+        k[slot // BS, :, slot % BS, D - 1] = -float("inf")
+    got = to_f64(binding.decode_split_sinks(q, k, v, tables, lens, 0.1, window, sinks,
+                                            partition_tokens=PARTITION[way])[:9])
+    assert np.all(np.isfinite(got)) and np.all(got[2] == 0) and np.all(got[5] == 0)
+    t = np.arange(CTX)
+    for s in (0, 1, 3, 4, 6, 7):
+        see = (t >= CTX - window) | (t < sinks)
+        see[list(BAD_KEYS.get(s, []))] = False
+        slot = slots_of(own, s, t[see])
+        K, V = (to_f64(x)[slot // BS, :, slot % BS] for x in (k, v))
+        for h in range(Hq):
+            want = attention_definition(to_f64(q[s, h]), K[:, h // (Hq // Hkv)], V[:, h // (Hq // Hkv)], 0.1)
+            limit = F32_MAX_ABS if dtype == torch.float32 else BF16_MAX_ABS
+            assert np.abs(got[s, h] - want).max() <= limit, (s, h)
