@@ -252,7 +252,8 @@ def decode(q, k_pool, v_pool, block_tables, context_lens, scale: float, out=None
     """pa_decode: out[s, h] = softmax(scale * K_s q[s, h]) V_s over the paged cache."""
     torch = _torch()
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating_for(stream):
+            out = torch.empty_like(q)
     B, Hq, D, NB, Hkv, BS, MBS = _decode_common(q, k_pool, v_pool, block_tables, context_lens, out)
     _check(library().pa_decode(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens), B, Hq, Hkv,
@@ -293,7 +294,8 @@ def decode_split(q, k_pool, v_pool, block_tables, context_lens, scale: float,
     """pa_decode_split: the same result via context partitions and an LSE merge."""
     torch = _torch()
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating_for(stream):
+            out = torch.empty_like(q)
     B, Hq, D, NB, Hkv, BS, MBS = _decode_common(q, k_pool, v_pool, block_tables, context_lens, out)
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
@@ -310,7 +312,8 @@ def decode_split_window(q, k_pool, v_pool, block_tables, context_lens, scale: fl
     """pa_decode_split_window: attention over the last ``window`` tokens only."""
     torch = _torch()
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating_for(stream):
+            out = torch.empty_like(q)
     B, Hq, D, NB, Hkv, BS, MBS = _decode_common(q, k_pool, v_pool, block_tables, context_lens, out)
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
@@ -346,12 +349,13 @@ def swap_in(host_k, host_v, k_pool, v_pool, pairs, dev_err=None, stream=None):
 
 
 def prefill_workspace(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim, block_size,
-                      max_blocks_per_seq, partition_tokens, device=None) -> "Workspace":
+                      max_blocks_per_seq, partition_tokens, device=None,
+                      stream=None) -> "Workspace":
     n = library().pa_prefill_workspace_size(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim,
                                             block_size, max_blocks_per_seq, partition_tokens)
     if n == 0:
         raise InvalidArgumentError(PA_ERR_INVALID_ARG, "bad workspace size arguments")
-    return Workspace(n, device)
+    return Workspace(n, device, stream)
 
 
 def prefill(q, k_pool, v_pool, block_tables, context_lens, query_lens, scale: float,
@@ -363,7 +367,8 @@ def prefill(q, k_pool, v_pool, block_tables, context_lens, query_lens, scale: fl
     torch = _torch()
     _require_cuda(q, k_pool, v_pool, block_tables)
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating_for(stream):
+            out = torch.empty_like(q)
     ctx = np.ascontiguousarray(np.asarray(context_lens, dtype=np.int32))
     qlen = np.ascontiguousarray(np.asarray(query_lens, dtype=np.int32))
     total, Hq, D = q.shape
@@ -372,7 +377,8 @@ def prefill(q, k_pool, v_pool, block_tables, context_lens, query_lens, scale: fl
     if block_tables.dtype != torch.int32 or ctx.shape != (B,) or qlen.shape != (B,):
         raise InvalidArgumentError(PA_ERR_INVALID_ARG, "bad tables or length arrays")
     if workspace is None:
-        workspace = prefill_workspace(B, total, Hq, Hkv, D, BS, MBS, partition_tokens, q.device)
+        workspace = prefill_workspace(B, total, Hq, Hkv, D, BS, MBS, partition_tokens, q.device,
+                                      stream)
     _check(library().pa_prefill(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), ctx.ctypes.data, qlen.ctypes.data,
         B, total, Hq, Hkv, D, BS, NB, MBS, float(scale), _dtype_code(q), int(partition_tokens),
@@ -402,25 +408,28 @@ def prefill_plan(context_lens, query_lens, num_q_heads: int, num_kv_heads: int, 
 
 class Workspace:
     """Caller-owned, 256-byte aligned device workspace, zeroed once (the
-    contract of pa_decode_split_workspace_init)."""
+    contract of pa_decode_split_workspace_init) on ``stream``, whose calls may
+    then use it."""
 
     def __init__(self, nbytes: int, device=None, stream=None):
         torch = _torch()
         self.nbytes = int(nbytes)
-        self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8,
-                                  device=device or torch.device("cuda"))
+        with _allocating_for(stream):
+            self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8,
+                                      device=device or torch.device("cuda"))
         self.ptr = (self.buffer.data_ptr() + 255) & ~255
         _check(library().pa_decode_split_workspace_init(self.ptr, self.nbytes, _stream_ptr(stream)))
 
 
 def shared_prefix_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
-                            max_blocks_per_seq, partition_tokens, device=None) -> Workspace:
+                            max_blocks_per_seq, partition_tokens, device=None,
+                            stream=None) -> Workspace:
     n = library().pa_decode_shared_prefix_workspace_size(
         num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
         partition_tokens)
     if n == 0:
         raise InvalidArgumentError(PA_ERR_INVALID_ARG, "bad workspace size arguments")
-    return Workspace(n, device)
+    return Workspace(n, device, stream)
 
 
 def decode_shared_prefix(q, k_pool, v_pool, block_tables, context_lens, scale: float, groups,
@@ -431,11 +440,13 @@ def decode_shared_prefix(q, k_pool, v_pool, block_tables, context_lens, scale: f
     import numpy as np
     torch = _torch()
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating_for(stream):
+            out = torch.empty_like(q)
     B, Hq, D, NB, Hkv, BS, MBS = _decode_common(q, k_pool, v_pool, block_tables, context_lens, out)
     offs, members, blocks = (np.ascontiguousarray(np.asarray(x, dtype=np.int32)) for x in groups)
     if workspace is None:
-        workspace = shared_prefix_workspace(B, Hq, Hkv, D, BS, MBS, partition_tokens, q.device)
+        workspace = shared_prefix_workspace(B, Hq, Hkv, D, BS, MBS, partition_tokens, q.device,
+                                            stream)
     _check(library().pa_decode_shared_prefix(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens), B, Hq, Hkv,
         D, BS, NB, MBS, float(scale), _dtype_code(q), int(partition_tokens), int(blocks.shape[0]),
