@@ -501,6 +501,16 @@ def _on_device(*tensors):
             raise _bad("tensors must be contiguous and on the current CUDA device")
 
 
+def _err_ptr(dev_err):
+    """Address of an error word: kernels write to it, so it is looked at like the rest."""
+    if dev_err is None:
+        return 0
+    _on_device(dev_err)
+    if dev_err.element_size() != 4 or dev_err.numel() < 1:
+        raise _bad("dev_err must be a 32-bit word")
+    return dev_err.data_ptr()
+
+
 def _token_rows(t, heads, head_dim, what):
     """Elements between the tokens of a [tokens, heads, head_dim] tensor whose
     heads and dims are contiguous (a slice of a fused product, or whole)."""
@@ -522,12 +532,15 @@ def decode_split_sinks(q, k_pool, v_pool, block_tables, context_lens, scale: flo
         with _allocating_for(stream):
             out = torch.empty_like(q)
     B, Hq, D, NB, Hkv, BS, MBS = _decode_common(q, k_pool, v_pool, block_tables, context_lens, out)
+    _on_device(q, k_pool, v_pool, block_tables, context_lens, out)
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
+    else:
+        _on_device(workspace.buffer)
     _check(library().pa_decode_split_sinks(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens), B, Hq, Hkv,
         D, BS, NB, MBS, float(scale), _dtype_code(q), workspace.partition_tokens, int(window),
-        int(sinks), workspace.ptr, workspace.nbytes, _ptr(out), _ptr(dev_err),
+        int(sinks), workspace.ptr, workspace.nbytes, _ptr(out), _err_ptr(dev_err),
         _stream_ptr(stream)))
     return out
 
@@ -579,7 +592,7 @@ def kv_append_q4(k_new, v_new, slot_mapping, k_pool, v_pool, dev_err=None, strea
     _check(library().pa_kv_append_q4(
         k_new.data_ptr(), v_new.data_ptr(), _token_rows(k_new, Hkv, D, "k_new"),
         _token_rows(v_new, Hkv, D, "v_new"), slot_mapping.data_ptr(), T, Hkv, D, BS, NB,
-        _dtype_code(k_new), k_pool.data_ptr(), v_pool.data_ptr(), _ptr(dev_err),
+        _dtype_code(k_new), k_pool.data_ptr(), v_pool.data_ptr(), _err_ptr(dev_err),
         _stream_ptr(stream)))
 
 
@@ -606,7 +619,7 @@ def kv_gather_q4(k_pool, v_pool, slot_mapping, head_dim: int, dtype=None, out=No
             raise _bad("out must be two [tokens, heads, head_dim] tensors of one type")
     _check(library().pa_kv_gather_q4(
         k_pool.data_ptr(), v_pool.data_ptr(), slot_mapping.data_ptr(), T, Hkv, int(head_dim), BS,
-        NB, _dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(), _ptr(dev_err),
+        NB, _dtype_code(k_out), k_out.data_ptr(), v_out.data_ptr(), _err_ptr(dev_err),
         _stream_ptr(stream)))
     return k_out, v_out
 
@@ -631,11 +644,13 @@ def decode_q4(q, k_pool, v_pool, block_tables, context_lens, scale: float, windo
         raise _bad("out must match q")
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
+    else:
+        _on_device(workspace.buffer)
     _check(library().pa_decode_q4(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
         context_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, MBS, float(scale), _dtype_code(q),
         int(window), int(sinks), workspace.partition_tokens, workspace.ptr, workspace.nbytes,
-        out.data_ptr(), _ptr(dev_err), _stream_ptr(stream)))
+        out.data_ptr(), _err_ptr(dev_err), _stream_ptr(stream)))
     return out
 
 
@@ -701,7 +716,7 @@ def rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_pool, v_po
               positions.data_ptr(), inv_freq.data_ptr(), slot_mapping.data_ptr(), T, Hq, Hkv, D,
               2 * inv_freq.size(0), 1 if interleaved else 0, float(mscale), BS, NB,
               _dtype_code(k_new),
-              out_ptr, k_pool.data_ptr(), v_pool.data_ptr(), _ptr(dev_err), _stream_ptr(stream)))
+              out_ptr, k_pool.data_ptr(), v_pool.data_ptr(), _err_ptr(dev_err), _stream_ptr(stream)))
     return q_out if q is not None else None
 
 
@@ -753,7 +768,7 @@ def extend_tables(block_tables, context_lens, new_lens, free_queue, queue_state,
         block_tables.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(), B, MBS,
         int(block_size), free_queue.data_ptr(), free_queue.numel(), queue_state.data_ptr(),
         int(max_tokens), lens.data_ptr(), start.data_ptr(), pos.data_ptr(), slots.data_ptr(),
-        state.data_ptr(), _ptr(dev_err), _stream_ptr(stream)))
+        state.data_ptr(), _err_ptr(dev_err), _stream_ptr(stream)))
     return out
 
 
