@@ -33,6 +33,7 @@ class OnDevice:
 @pytest.fixture(autouse=True)
 def device_zero_is_current(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(binding, "_stream_ptr", lambda stream: 0)
 
     class NoLibrary:
         def __getattr__(self, name):
