@@ -606,7 +606,7 @@ pa_status_t run_rope(RopeArgs p, int head_dim, bool interleaved, int num_blocks,
     return fail(PA_ERR_UNSUPPORTED, "too many heads");
   if (p.num_q_heads > 0) {
     // q_out may be q itself (each thread writes what it alone has read), and
-    // nothing else that the call reads.
+    // nothing else that the call reads or writes: CTAs run in any order.
     const size_t n = static_cast<size_t>(p.num_tokens), last = n - 1;
     const size_t out = n * qrow * eb;
     const bool same = p.q == p.q_out && p.q_stride == qrow;
@@ -614,6 +614,13 @@ pa_status_t run_rope(RopeArgs p, int head_dim, bool interleaved, int num_blocks,
         overlap(p.q_out, out, p.k, (last * p.k_stride + krow) * eb) ||
         overlap(p.q_out, out, p.v, (last * p.v_stride + krow) * eb))
       return fail(PA_ERR_INVALID_ARG, "q_out overlaps an input (it may only be q itself, contiguous)");
+    const size_t pool = q4 ? static_cast<size_t>(num_blocks) * p.num_kv_heads * pa_q4_tile_bytes(p.block_size, head_dim)
+                           : static_cast<size_t>(num_blocks) * p.block_size * krow * eb;
+    if (overlap(p.q_out, out, p.k_pool, pool) || overlap(p.q_out, out, p.v_pool, pool) ||
+        overlap(p.q_out, out, p.slots, n * 8) ||
+        (p.rotary_dim > 0 && (overlap(p.q_out, out, p.positions, n * 4) ||
+                              overlap(p.q_out, out, p.inv_freq, static_cast<size_t>(p.rotary_dim) * 2))))
+      return fail(PA_ERR_INVALID_ARG, "q_out overlaps a pool, the slots, the positions or the frequencies");
   }
   p.num_slots = static_cast<int64_t>(num_blocks) * p.block_size;
   p.block_shift = p.block_size == 16 ? 4 : 5;
@@ -737,6 +744,13 @@ pa_status_t pa_kv_gather_q4(const void* k_pool, const void* v_pool, const int64_
   if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_out) || !aligned16(v_out))
     return fail(PA_ERR_INVALID_ARG, "pools and outputs must be 16-byte aligned");
   const int64_t slots = static_cast<int64_t>(num_blocks) * block_size;
+  const size_t out = static_cast<size_t>(num_tokens) * num_kv_heads * head_dim * (dtype == PA_F32 ? 4 : 2);
+  const size_t pool = static_cast<size_t>(num_blocks) * num_kv_heads * pa_q4_tile_bytes(block_size, head_dim);
+  const size_t row_slots = static_cast<size_t>(num_tokens) * 8;
+  if (overlap(k_out, out, v_out, out)) return fail(PA_ERR_INVALID_ARG, "k_out and v_out share memory");
+  for (const void* o : {k_out, v_out})
+    if (overlap(o, out, k_pool, pool) || overlap(o, out, v_pool, pool) || overlap(o, out, slot_mapping, row_slots))
+      return fail(PA_ERR_INVALID_ARG, "an output shares memory with a pool or the slots");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto go = [&](auto elt) {
     using T = decltype(elt);
