@@ -472,9 +472,11 @@ pa_status_t pa_kv_gather_q4(const void* k_pool, const void* v_pool, const int64_
  * Arithmetic: queries enter as 16-bit whole numbers relative to the largest
  * |q| of their head (off by at most 2^-15 of it), multiplied with the codes
  * exactly; logits, softmax sums and minima are fp32; softmax weights times the
- * values' scales are rounded to f16 (11 bits) before the product with the
- * value codes. Key scales up to 2^100; value scales up to 2^61, and below
- * 2^-54 with fewer than 11 bits.
+ * values' scales are rounded to f16 before the product with the value codes:
+ * 11 bits, or 2^-39 of the sequence's largest weight times its 64-dim group's
+ * largest scale where that is more. Key scales up to 2^100; values up to 2^96
+ * hold for any length (sums over the tokens are fp32, as in the 16-bit calls).
+ * A visible NaN makes its heads (in the values: its group's dims) NaN.
  *
  * workspace, partition_tokens: the contract of pa_decode_split with the same
  * sizes; large batches are cut as for its long tables (equal runs of 16-token

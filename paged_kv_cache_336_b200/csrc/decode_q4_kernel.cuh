@@ -37,11 +37,11 @@
 //   they cost conversions and two f16 products each.
 // * O: codes less 8 as f16 (CodeBits) against p s in f16, transposed between
 //   its two layouts by movmatrix. f16 needs the weights' range bounded: see
-//   Q4Warp::expo. In exchange O accumulates in place, where a mask-or'ed bf16
+//   Q4Warp::up. In exchange O accumulates in place, where a mask-or'ed bf16
 //   code (128 + c) would leave a cancellation of 128 to a few.
 // * A step (64 tokens at head_dim 128, 128 at 64, 48 at 256) shares one running
-//   maximum; the accumulators are rescaled only when it (or expo) moves. Steps
-//   that are not whole go unit by unit through the masked build.
+//   maximum; the accumulators are rescaled only when it (or a group's up) moves.
+//   Steps that are not whole go unit by unit through the masked build.
 // Rounding: q to 16 bits of its head's range (at most 2^-15 of the largest),
 // p s to f16 (2^-11), the output to bf16; sums, logits, minima in fp32 or exact.
 // Bound: 8 x 131072 tokens (64 heads over 8, head_dim 128) take 250 us, 1.21 GB
@@ -190,23 +190,23 @@ struct Q4Warp {
   static constexpr int D = Cfg::D;
   static constexpr int US = Cfg::US;
   static constexpr int GR = Geo::kGroups;
-  // expo's range: scales up to 2^61; those below 2^-40 keep f16's 11 bits down
-  // to 2^-68, and pieces merged by 2^(m - M) stay within fp32's exponents.
-  static constexpr int kMinExpo = -40, kMaxExpo = 60;
 
   // Query operand: rint(2^k q), 16 bits, as high bytes (signed) and low bytes
   // (unsigned) per octet of 8 dims that the lane holds (even dims, odd dims).
   uint32_t qb[GR][2][2][2];
   float qs[GR][2];        // 2^k Q_i of heads 2t, 2t + 1
   float f[2];             // |scale| log2(e) 2^-k of heads 2t, 2t + 1
-  float o[GR][4][4];      // O^T: dims 64 i + 8 g + 2 j (+ 1 for e >= 2), head 2t + (e & 1)
+  float o[GR][4][4];      // up[i] times O^T: dims 64 i + 8 g + 2 j (+ 1 for e >= 2), head 2t + (e & 1)
   float mid[GR][2];       // sum p (mn + 8 s) over this lane's tokens
-  // Softmax weights are held as 2^(y - m), m = top + expo - 14, with top the
-  // running maximum of the logits y (log2 domain) and 2^expo the largest power
-  // of two of the value scales met: then a weight times a scale is below 2^15
-  // and fits f16 with 39 binades to spare below.
-  float top[2], m[2], l[2];  // l: this lane's part of the sum
-  int expo;
+  // Softmax weights are p = 2^(y - m), m the running maximum of the logits y (log2
+  // domain). A weight times a value scale enters O's products as f16, so group i's
+  // scales are taken times up[i] = 2^(14 - e), with 2^e the largest power of two
+  // among those met: products below 2^15, 11 bits down to 2^-28 of the largest
+  // weight times the group's largest scale and 2^-39 of that apart below.
+  // A power for each group, and none in mid, because groups may differ by any
+  // factor, and minima by any factor from scales.
+  float m[2], l[2];       // l: this lane's part of the sum
+  float up[GR];
   // This lane's places in a sub-tile. K: its row (rows g and g + 8 of S are
   // tokens tok and tok + 8); V: tokens t and 7 - t (+ 8); both: parameters.
   CodeBits bits;
@@ -244,11 +244,11 @@ struct Q4Warp {
     largest = max_nan(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
     // k brings the row's largest |q| into [2^14, 2^15); q of a negative scale is negated
     const int e = max(static_cast<int>(__float_as_uint(largest) >> 23), 16);
-    const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);   // 2^k, k = 141 - e
+    const float pow_k = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);  // 2^k, k = 141 - e
     const float down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);  // 2^-k
     float fac = fabsf(scale_log2) * down;
     if (!(largest < INFINITY)) fac = __uint_as_float(0x7fc00000u);
-    const float sgn = scale_log2 < 0.f ? -up : up;
+    const float sgn = scale_log2 < 0.f ? -pow_k : pow_k;
 #pragma unroll
     for (int i = 0; i < GR; ++i) {
       float sum = 0.f;
@@ -275,14 +275,14 @@ struct Q4Warp {
       qs[i][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
       qs[i][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
       mid[i][0] = mid[i][1] = 0.f;
+      up[i] = 0x1p126f;  // (a scale of 2^-111 or more asks for less)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
     }
     f[0] = __shfl_sync(0xffffffffu, fac, 8 * t);
     f[1] = __shfl_sync(0xffffffffu, fac, 8 * t + 4);
-    top[0] = top[1] = m[0] = m[1] = -INFINITY;
+    m[0] = m[1] = kNoTokens;
     l[0] = l[1] = 0.f;
-    expo = kMinExpo;
   }
 
   // A step is logits() and then attend(), over NU units whose sub-tiles lie one
@@ -344,9 +344,9 @@ struct Q4Warp {
   template <int NU, bool kEdge>
   __device__ __forceinline__ void attend(uint32_t v_tile, float (&x)[NU][4], const bool (&out)[2]) {
     const uint32_t v_par = v_tile + par_at;
-    // ---- a value scale of 2^(expo + 1) or more asks for a larger expo (a NaN or an
-    // infinity only comes by here) ------------------------------------------------------
-    uint32_t smax = 0;
+    // ---- a value scale that up[] would take to 2^15 or more asks for less. (A NaN
+    // hides the group's other scales: its values are NaN anyway.) ---------------------
+    uint32_t smax[GR] = {};
 #pragma unroll
     for (int u = 0; u < NU; ++u)
 #pragma unroll
@@ -354,9 +354,12 @@ struct Q4Warp {
         uint32_t par[GR];
         lds_words(v_par + u * Geo::kSubBytes + 8 * r * Geo::kParamRow, par);
 #pragma unroll
-        for (int i = 0; i < GR; ++i) smax = __vmaxu2(smax, out[r] ? 0u : par[i]);
+        for (int i = 0; i < GR; ++i) smax[i] = __vmaxu2(smax[i], out[r] ? 0u : par[i]);
       }
-    if (__any_sync(0xffffffffu, (smax & 0xffffu) >= static_cast<uint32_t>(expo + 128) << 7)) raise_expo<NU>(v_par, out);
+    bool large = false;
+#pragma unroll
+    for (int i = 0; i < GR; ++i) large |= bf16_lo(smax[i]) * up[i] >= 0x1p15f;
+    if (__any_sync(0xffffffffu, large)) lower_up<NU>(v_par, out);
     // ---- running softmax over the step's tokens ------------------------------------
     float ref[2];
 #pragma unroll
@@ -366,10 +369,9 @@ struct Q4Warp {
       for (int u = 1; u < NU; ++u) mx = fmaxf(mx, fmaxf(x[u][h], x[u][2 + h]));
 #pragma unroll
       for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      top[h] = fmaxf(top[h], kEdge ? mx : mx * f[h]);
-      ref[h] = top[h] + static_cast<float>(expo - 14);
+      ref[h] = fmaxf(m[h], kEdge ? mx : mx * f[h]);
     }
-    if (__any_sync(0xffffffffu, ref[0] != m[0] || ref[1] != m[1])) {  // (a NaN differs too)
+    if (__any_sync(0xffffffffu, ref[0] != m[0] || ref[1] != m[1])) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float alpha = fast_exp2(m[h] - ref[h]);
@@ -403,8 +405,8 @@ struct Q4Warp {
         for (int i = 0; i < GR; ++i) {
           if (out[r]) par[i] = 0u;
           const float sc = bf16_lo(par[i]);
-          const float mi = fmaf(8.f, sc, bf16_hi(par[i]));
-          pb[u][i][r] = movmatrix(pack_f16x2(p[2 * r] * sc, p[2 * r + 1] * sc));
+          const float mi = fmaf(8.f, sc, bf16_hi(par[i])), su = sc * up[i];
+          pb[u][i][r] = movmatrix(pack_f16x2(p[2 * r] * su, p[2 * r + 1] * su));
           mid[i][0] = fmaf(p[2 * r], mi, mid[i][0]);
           mid[i][1] = fmaf(p[2 * r + 1], mi, mid[i][1]);
         }
@@ -435,10 +437,11 @@ struct Q4Warp {
     }
   }
 
-  // The largest exponent of the step's finite value scales becomes expo.
+  // up[i] falls to 2^(14 - e), with e the largest exponent of the step's finite
+  // scales of group i, and the group's sums with it.
   template <int NU>
-  __device__ __forceinline__ void raise_expo(uint32_t v_par, const bool (&out)[2]) {
-    uint32_t big = 0;
+  __device__ __forceinline__ void lower_up(uint32_t v_par, const bool (&out)[2]) {
+    uint32_t big[GR] = {};  // biased exponents
 #pragma unroll 1
     for (int u = 0; u < NU; ++u)
 #pragma unroll
@@ -448,16 +451,33 @@ struct Q4Warp {
 #pragma unroll
         for (int i = 0; i < GR; ++i) {
           const uint32_t e = (par[i] >> 7) & 0xffu;
-          if (!out[r] && e < 255u) big = max(big, e);
+          if (!out[r] && e < 255u) big[i] = max(big[i], e);
         }
       }
-    big = __reduce_max_sync(0xffffffffu, big);
-    expo = max(expo, min(static_cast<int>(big) - 127, kMaxExpo));
+#pragma unroll
+    for (int i = 0; i < GR; ++i) {
+      const int old = static_cast<int>(__float_as_uint(up[i]) >> 23);  // 14 .. 253
+      const int now = min(old, 268 - static_cast<int>(max(__reduce_max_sync(0xffffffffu, big[i]), 15u)));
+      up[i] = __uint_as_float(static_cast<uint32_t>(now) << 23);
+      const float by = __uint_as_float(static_cast<uint32_t>(max(127 + now - old, 0)) << 23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][j][e] *= by;
+    }
   }
 
-  // Completes the sums over lanes; then head 2t + h's dims 64 i + 8 g + 0..7 are
-  // value(i, h, 0..7).
+  // Completes the sums over lanes and takes up[] back; then head 2t + h's dims
+  // 64 i + 8 g + 0..7 are value(i, h, 0..7).
   __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int i = 0; i < GR; ++i) {
+      const float down = __uint_as_float((254u << 23) - __float_as_uint(up[i]));  // 1 / up[i]
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][j][e] *= down;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -482,9 +502,7 @@ struct Q4Warp {
   }
   __device__ __forceinline__ void store_partial(const DecodeArgs& a, int64_t pr, int h, int g) const {
     if (g == 0) {
-      // a piece without a token (bad block ids) weighs nothing; -inf would make
-      // the merge of nothing but such pieces a NaN
-      a.part_m[pr] = m[h] == -INFINITY ? kNoTokens : m[h];
+      a.part_m[pr] = m[h];
       a.part_l[pr] = l[h];
     }
 #pragma unroll
@@ -790,7 +808,7 @@ __device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, cons
   const Q4Run run = q4_run<Cfg>(a, lists, prefix, q_tiles, warp);
   Q4Warp<Cfg> st;
   st.places(lane);
-  st.m[0] = st.m[1] = -INFINITY;
+  st.m[0] = st.m[1] = kNoTokens;
   q4_walk<Cfg>(a, run, st, prefix, first_unit, ring, full, empty, present);
   if (a.seq_cut <= 1) return;
   // ---- pieces of one sequence, merged in shared memory: every consumer comes
@@ -822,11 +840,10 @@ __device__ __forceinline__ void q4_consume(const SinksArgs& a, int q_tiles, cons
   if (run.seq >= a.num_seqs) return;
   const int heads = min(8, a.group - 8 * run.qt), w0 = warp - run.piece;
   for (int hd = run.piece; hd < heads; hd += a.seq_cut) {
-    float top = -INFINITY;
+    // A piece whose logits are all NaN has the maximum of one without a token
+    // (fmaxf passes over NaN), but sums of NaN, which any weight keeps.
+    float top = kNoTokens;
     for (int p = 0; p < a.seq_cut; ++p) top = fmaxf(top, state(w0 + p)[8 * D + hd]);
-    // A maximum of -inf does not tell a piece without a token from one whose logits
-    // are all NaN (which fmaxf passes over): the latter weighs 0, and 0 * NaN is NaN.
-    if (top == -INFINITY) top = 0.f;
     float sum = 0.f, acc[D / 32];
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
