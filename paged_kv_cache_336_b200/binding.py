@@ -232,8 +232,12 @@ def _require_cuda(*tensors):
 
 
 def _decode_common(q, k_pool, v_pool, block_tables, context_lens, out):
-    torch = _torch()
     _require_cuda(q, k_pool, v_pool, block_tables, context_lens, out)
+    return _decode_shapes(q, k_pool, v_pool, block_tables, context_lens, out)
+
+
+def _decode_shapes(q, k_pool, v_pool, block_tables, context_lens, out):
+    torch = _torch()
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise InvalidArgumentError(PA_ERR_INVALID_ARG, "block_tables and context_lens must be int32")
     if not (q.dtype == k_pool.dtype == v_pool.dtype == out.dtype):
@@ -531,12 +535,12 @@ def decode_split_sinks(q, k_pool, v_pool, block_tables, context_lens, scale: flo
     if out is None:
         with _allocating_for(stream):
             out = torch.empty_like(q)
-    B, Hq, D, NB, Hkv, BS, MBS = _decode_common(q, k_pool, v_pool, block_tables, context_lens, out)
     _on_device(q, k_pool, v_pool, block_tables, context_lens, out)
+    B, Hq, D, NB, Hkv, BS, MBS = _decode_shapes(q, k_pool, v_pool, block_tables, context_lens, out)
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
-    else:
-        _on_device(workspace.buffer)
+    elif workspace.buffer.get_device() != q.get_device():
+        raise _bad("the workspace must be on the tensors' device")
     _check(library().pa_decode_split_sinks(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens), B, Hq, Hkv,
         D, BS, NB, MBS, float(scale), _dtype_code(q), workspace.partition_tokens, int(window),
@@ -644,8 +648,8 @@ def decode_q4(q, k_pool, v_pool, block_tables, context_lens, scale: float, windo
         raise _bad("out must match q")
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
-    else:
-        _on_device(workspace.buffer)
+    elif workspace.buffer.get_device() != q.get_device():
+        raise _bad("the workspace must be on the tensors' device")
     _check(library().pa_decode_q4(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
         context_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, MBS, float(scale), _dtype_code(q),
