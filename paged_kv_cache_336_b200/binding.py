@@ -515,6 +515,12 @@ def _err_ptr(dev_err):
     return dev_err.data_ptr()
 
 
+def _span(n):
+    """A window or a number of sinks as a C int, which ctypes would wrap: what no
+    context reaches is all alike, and so is what is refused."""
+    return max(-1, min(int(n), 0x7fffffff))
+
+
 def _token_rows(t, heads, head_dim, what):
     """Elements between the tokens of a [tokens, heads, head_dim] tensor whose
     heads and dims are contiguous (a slice of a fused product, or whole)."""
@@ -543,8 +549,8 @@ def decode_split_sinks(q, k_pool, v_pool, block_tables, context_lens, scale: flo
         raise _bad("the workspace must be on the tensors' device")
     _check(library().pa_decode_split_sinks(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens), B, Hq, Hkv,
-        D, BS, NB, MBS, float(scale), _dtype_code(q), workspace.partition_tokens, int(window),
-        int(sinks), workspace.ptr, workspace.nbytes, _ptr(out), _err_ptr(dev_err),
+        D, BS, NB, MBS, float(scale), _dtype_code(q), workspace.partition_tokens, _span(window),
+        _span(sinks), workspace.ptr, workspace.nbytes, _ptr(out), _err_ptr(dev_err),
         _stream_ptr(stream)))
     return out
 
@@ -653,7 +659,7 @@ def decode_q4(q, k_pool, v_pool, block_tables, context_lens, scale: float, windo
     _check(library().pa_decode_q4(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
         context_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, MBS, float(scale), _dtype_code(q),
-        int(window), int(sinks), workspace.partition_tokens, workspace.ptr, workspace.nbytes,
+        _span(window), _span(sinks), workspace.partition_tokens, workspace.ptr, workspace.nbytes,
         out.data_ptr(), _err_ptr(dev_err), _stream_ptr(stream)))
     return out
 
