@@ -515,6 +515,14 @@ def _err_ptr(dev_err):
     return dev_err.data_ptr()
 
 
+def _dims(t, rank, what):
+    """The shape of a tensor of `rank` dims."""
+    shape = t.shape
+    if len(shape) != rank:
+        raise _bad(f"{what} must have {rank} dimensions, not {len(shape)}")
+    return shape
+
+
 def _span(n):
     """A window or a number of sinks as a C int, which ctypes would wrap: what no
     context reaches is all alike, and so is what is refused."""
@@ -580,7 +588,7 @@ def _q4_pool_shape(k_pool, v_pool, head_dim):
             or k_pool.shape != v_pool.shape):
         raise _bad("4-bit pools must be two uint8 [num_blocks, num_kv_heads, tile bytes] tensors")
     NB, Hkv, tile = k_pool.shape
-    BS = 16 * tile // (9 * head_dim)
+    BS = 16 * tile // (9 * head_dim) if head_dim > 0 else 0
     if BS < 16 or tile != BS // 16 * 9 * head_dim:
         raise _bad(f"tiles of {tile} bytes do not hold blocks of head_dim {head_dim}")
     return NB, Hkv, BS
@@ -590,7 +598,7 @@ def kv_append_q4(k_new, v_new, slot_mapping, k_pool, v_pool, dev_err=None, strea
     """pa_kv_append_q4: quantises new rows (bf16, heads and dims contiguous)
     into their slots of 4-bit pools."""
     torch = _torch()
-    shape = T, Hkv, D = k_new.shape
+    shape = T, Hkv, D = _dims(k_new, 3, "k_new")
     NB, H2, BS = _q4_pool_shape(k_pool, v_pool, D)
     _on_device(k_pool, v_pool, slot_mapping)
     dev = k_pool.get_device()
@@ -643,10 +651,10 @@ def decode_q4(q, k_pool, v_pool, block_tables, context_lens, scale: float, windo
     if out is None:
         with _allocating_for(stream):
             out = torch.empty_like(q)
-    shape = B, Hq, D = q.shape
+    shape = B, Hq, D = _dims(q, 3, "q")
     NB, Hkv, BS = _q4_pool_shape(k_pool, v_pool, D)
     _on_device(q, k_pool, v_pool, block_tables, context_lens, out)
-    rows, MBS = block_tables.shape
+    rows, MBS = _dims(block_tables, 2, "block_tables")
     if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or rows != B
             or context_lens.shape != (B,)):
         raise _bad("block_tables must be int32 [seqs, blocks], context_lens int32 [seqs]")
@@ -687,13 +695,13 @@ def rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_pool, v_po
     and k by their positions and writes k and v into their slots. q may be
     None; returns the rotated queries (None without q)."""
     torch = _torch()
-    shape = T, Hkv, D = k_new.shape
+    shape = T, Hkv, D = _dims(k_new, 3, "k_new")
     dtype = k_new.dtype
     q4 = k_pool.dtype == torch.uint8
     if q4:
         NB, H2, BS = _q4_pool_shape(k_pool, v_pool, D)
     else:
-        NB, H2, BS, D2 = k_pool.shape
+        NB, H2, BS, D2 = _dims(k_pool, 4, "16-bit pools")
         if D2 != D or v_pool.shape != k_pool.shape:
             raise _bad("pools must be [num_blocks, num_kv_heads, block_size, head_dim]")
         if k_pool.dtype != dtype or v_pool.dtype != dtype:
@@ -709,7 +717,7 @@ def rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_pool, v_po
         raise _bad("k_new and v_new must match in shape, type and device")
     Hq = q_stride = q_ptr = out_ptr = 0
     if q is not None:
-        rows, Hq, Dq = q.shape
+        rows, Hq, Dq = _dims(q, 3, "q")
         if rows != T or Dq != D or q.dtype != dtype or q.get_device() != dev:
             raise _bad("q must have the tokens, head_dim, type and device of k_new")
         q_stride = _token_rows(q, Hq, D, "q")
@@ -757,7 +765,7 @@ def extend_tables(block_tables, context_lens, new_lens, free_queue, queue_state,
     returns its StepTables. ``out`` shares nothing with the inputs: a loop keeps
     two and swaps them."""
     torch = _torch()
-    B, MBS = block_tables.shape
+    B, MBS = _dims(block_tables, 2, "block_tables")
     if out is None:
         with _allocating_for(stream):
             out = StepTables.empty(B, max_tokens, block_tables.device)
