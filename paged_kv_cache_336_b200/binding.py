@@ -551,6 +551,8 @@ def decode_split_sinks(q, k_pool, v_pool, block_tables, context_lens, scale: flo
             out = torch.empty_like(q)
     _on_device(q, k_pool, v_pool, block_tables, context_lens, out)
     B, Hq, D, NB, Hkv, BS, MBS = _decode_shapes(q, k_pool, v_pool, block_tables, context_lens, out)
+    if B == 0:
+        return out
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
     elif workspace.buffer.get_device() != q.get_device():
@@ -660,6 +662,8 @@ def decode_q4(q, k_pool, v_pool, block_tables, context_lens, scale: float, windo
         raise _bad("block_tables must be int32 [seqs, blocks], context_lens int32 [seqs]")
     if out.shape != shape or out.dtype != q.dtype:
         raise _bad("out must match q")
+    if B == 0:
+        return out
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
     elif workspace.buffer.get_device() != q.get_device():
