@@ -286,6 +286,7 @@ class SplitWorkspace:
         with _allocating_for(stream):
             self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8,
                                       device=device or torch.device("cuda"))
+        self.device = self.buffer.get_device()
         base = self.buffer.data_ptr()
         self.ptr = (base + 255) & ~255
         _check(library().pa_decode_split_workspace_init(self.ptr, self.nbytes, _stream_ptr(stream)))
@@ -498,11 +499,12 @@ def _bad(msg):
 
 
 def _on_device(*tensors):
-    """Contiguous tensors on the current CUDA device."""
+    """Contiguous tensors on the current CUDA device, which is returned."""
     dev = _torch()._C._cuda_getDevice() if tensors[0].is_cuda else None
     for t in tensors:
         if t.get_device() != dev or not t.is_contiguous():
             raise _bad("tensors must be contiguous and on the current CUDA device")
+    return dev
 
 
 def _err_ptr(dev_err):
@@ -515,18 +517,11 @@ def _err_ptr(dev_err):
     return dev_err.data_ptr()
 
 
-def _dims(t, rank, what):
-    """The shape of a tensor of `rank` dims."""
-    shape = t.shape
-    if len(shape) != rank:
-        raise _bad(f"{what} must have {rank} dimensions, not {len(shape)}")
-    return shape
-
-
 def _span(n):
     """A window or a number of sinks as a C int, which ctypes would wrap: what no
     context reaches is all alike, and so is what is refused."""
-    return max(-1, min(int(n), 0x7fffffff))
+    n = int(n)
+    return n if 0 <= n <= 0x7fffffff else -1 if n < 0 else 0x7fffffff
 
 
 def _token_rows(t, heads, head_dim, what):
@@ -549,19 +544,19 @@ def decode_split_sinks(q, k_pool, v_pool, block_tables, context_lens, scale: flo
     if out is None:
         with _allocating_for(stream):
             out = torch.empty_like(q)
-    _on_device(q, k_pool, v_pool, block_tables, context_lens, out)
+    dev = _on_device(q, k_pool, v_pool, block_tables, context_lens, out)
     B, Hq, D, NB, Hkv, BS, MBS = _decode_shapes(q, k_pool, v_pool, block_tables, context_lens, out)
     if B == 0:
         return out
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
-    elif workspace.buffer.get_device() != q.get_device():
+    elif workspace.device != dev:
         raise _bad("the workspace must be on the tensors' device")
     _check(library().pa_decode_split_sinks(
-        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(context_lens), B, Hq, Hkv,
-        D, BS, NB, MBS, float(scale), _dtype_code(q), workspace.partition_tokens, _span(window),
-        _span(sinks), workspace.ptr, workspace.nbytes, _ptr(out), _err_ptr(dev_err),
-        _stream_ptr(stream)))
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, MBS, float(scale), _dtype_code(q),
+        workspace.partition_tokens, _span(window), _span(sinks), workspace.ptr, workspace.nbytes,
+        out.data_ptr(), _err_ptr(dev_err), _stream_ptr(stream)))
     return out
 
 
@@ -600,7 +595,10 @@ def kv_append_q4(k_new, v_new, slot_mapping, k_pool, v_pool, dev_err=None, strea
     """pa_kv_append_q4: quantises new rows (bf16, heads and dims contiguous)
     into their slots of 4-bit pools."""
     torch = _torch()
-    shape = T, Hkv, D = _dims(k_new, 3, "k_new")
+    try:
+        shape = T, Hkv, D = k_new.shape
+    except ValueError:
+        raise _bad("k_new must be [tokens, heads, head_dim]") from None
     NB, H2, BS = _q4_pool_shape(k_pool, v_pool, D)
     _on_device(k_pool, v_pool, slot_mapping)
     dev = k_pool.get_device()
@@ -653,10 +651,13 @@ def decode_q4(q, k_pool, v_pool, block_tables, context_lens, scale: float, windo
     if out is None:
         with _allocating_for(stream):
             out = torch.empty_like(q)
-    shape = B, Hq, D = _dims(q, 3, "q")
+    try:
+        shape = B, Hq, D = q.shape
+        rows, MBS = block_tables.shape
+    except ValueError:
+        raise _bad("q must be [seqs, heads, head_dim], block_tables [seqs, blocks]") from None
     NB, Hkv, BS = _q4_pool_shape(k_pool, v_pool, D)
-    _on_device(q, k_pool, v_pool, block_tables, context_lens, out)
-    rows, MBS = _dims(block_tables, 2, "block_tables")
+    dev = _on_device(q, k_pool, v_pool, block_tables, context_lens, out)
     if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or rows != B
             or context_lens.shape != (B,)):
         raise _bad("block_tables must be int32 [seqs, blocks], context_lens int32 [seqs]")
@@ -666,7 +667,7 @@ def decode_q4(q, k_pool, v_pool, block_tables, context_lens, scale: float, windo
         return out
     if workspace is None:
         workspace = SplitWorkspace(B, Hq, D, BS, MBS, partition_tokens, q.device, stream)
-    elif workspace.buffer.get_device() != q.get_device():
+    elif workspace.device != dev:
         raise _bad("the workspace must be on the tensors' device")
     _check(library().pa_decode_q4(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(),
@@ -699,13 +700,19 @@ def rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_pool, v_po
     and k by their positions and writes k and v into their slots. q may be
     None; returns the rotated queries (None without q)."""
     torch = _torch()
-    shape = T, Hkv, D = _dims(k_new, 3, "k_new")
+    try:
+        shape = T, Hkv, D = k_new.shape
+    except ValueError:
+        raise _bad("k_new must be [tokens, heads, head_dim]") from None
     dtype = k_new.dtype
     q4 = k_pool.dtype == torch.uint8
     if q4:
         NB, H2, BS = _q4_pool_shape(k_pool, v_pool, D)
     else:
-        NB, H2, BS, D2 = _dims(k_pool, 4, "16-bit pools")
+        try:
+            NB, H2, BS, D2 = k_pool.shape
+        except ValueError:
+            D2 = -1
         if D2 != D or v_pool.shape != k_pool.shape:
             raise _bad("pools must be [num_blocks, num_kv_heads, block_size, head_dim]")
         if k_pool.dtype != dtype or v_pool.dtype != dtype:
@@ -721,7 +728,10 @@ def rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_pool, v_po
         raise _bad("k_new and v_new must match in shape, type and device")
     Hq = q_stride = q_ptr = out_ptr = 0
     if q is not None:
-        rows, Hq, Dq = _dims(q, 3, "q")
+        try:
+            rows, Hq, Dq = q.shape
+        except ValueError:
+            raise _bad("q must be [tokens, heads, head_dim]") from None
         if rows != T or Dq != D or q.dtype != dtype or q.get_device() != dev:
             raise _bad("q must have the tokens, head_dim, type and device of k_new")
         q_stride = _token_rows(q, Hq, D, "q")
@@ -769,7 +779,10 @@ def extend_tables(block_tables, context_lens, new_lens, free_queue, queue_state,
     returns its StepTables. ``out`` shares nothing with the inputs: a loop keeps
     two and swaps them."""
     torch = _torch()
-    B, MBS = _dims(block_tables, 2, "block_tables")
+    try:
+        B, MBS = block_tables.shape
+    except ValueError:
+        raise _bad("block_tables must be [seqs, blocks]") from None
     if out is None:
         with _allocating_for(stream):
             out = StepTables.empty(B, max_tokens, block_tables.device)

@@ -45,7 +45,7 @@ def device_zero_is_current(monkeypatch):
 
 def workspace(device):
     ws = binding.SplitWorkspace.__new__(binding.SplitWorkspace)
-    ws.buffer, ws.ptr, ws.nbytes, ws.partition_tokens = OnDevice((1 << 20,), U8, device), 1 << 20, 1 << 20, 64
+    ws.device, ws.ptr, ws.nbytes, ws.partition_tokens = device, 1 << 20, 1 << 20, 64
     return ws
 
 
