@@ -281,7 +281,9 @@ pa_status_t pa_decode_split_window(const void* q, const void* k_pool, const void
  * a visible token, or with such logits only, gets zeros. A visible NaN makes its
  * heads NaN. fp32 and bf16, the shapes of pa_decode_split. Large
  * batches are cut as pa_decode_split cuts long tables, small ones sequence by
- * sequence. Same workspace and contract as pa_decode_split.
+ * sequence. Same workspace and contract as pa_decode_split, and the same
+ * arithmetic: with bf16 the softmax weights are rounded to bf16 before the
+ * product with the values (their sum is of the unrounded ones), all sums fp32.
  * ------------------------------------------------------------------------- */
 pa_status_t pa_decode_split_sinks(const void* q, const void* k_pool, const void* v_pool,
                                   const int32_t* block_tables, const int32_t* context_lens,
@@ -413,7 +415,8 @@ pa_status_t pa_copy_blocks(void* k_pool, void* v_pool, const int64_t* src_dst_pa
  *
  * The 64 dims 64 i .. 64 i + 63 of one (token, KV head) are a group:
  *     mn = min x,  s = bf16((max x - mn) / 15),
- *     code = rint((x - mn) / s) in 0..15 (ties to even; 0 when s = 0),
+ *     code = rint((x - mn) / s) in 0..15 (ties to even; 0 when s = 0; the
+ *            difference and the quotient rounded to fp32),
  *     value = mn + s * code.
  * x is bf16, so mn is exact in bf16. A group that holds a NaN or an infinity
  * gets s = mn = NaN: all of its values read NaN.
@@ -451,7 +454,7 @@ pa_status_t pa_kv_append_q4(const void* k_new, const void* v_new, int64_t k_stri
 /* ---------------------------------------------------------------------------
  * pa_kv_gather_q4 - reads rows of a 4-bit cache back: k_out, v_out
  * [num_tokens][num_kv_heads][head_dim] in dtype (PA_F32 or PA_BF16), row t the
- * values of slot_mapping[t] (rounded once for bf16). A row with a negative
+ * values of slot_mapping[t] (rounded to fp32, for bf16 then to bf16). A row with a negative
  * slot is left as it was. A slot may appear any number of times. The outputs
  * share no memory with one another, the pools or the slots. With slots
  * in token order it lays a sequence out for pa_prefill's 16-bit pools

@@ -30,6 +30,8 @@ static DecodeInstance make_q4() {
 // head_dim 256 needs 232 registers, so 8 warps; 4 x 131072 / 128 ragged:
 // 8 x 3 x 3 248 / 98 us; 8 x 2 x 4 258 / 105; 8 x 2 x 3 261 / 104; 8 x 4 x 2
 // 250 / 106 (and it spills).
+// (All with one power of two for the value scales; one for each group costs 1 to
+// 2%: 249 / 97 us at head_dim 128, 157 / 66 at 64, 253 / 100 at 256.)
 template <int BS>
 static bool pick(int head_dim, DecodeInstance* out) {
   if (head_dim == 64) { *out = make_q4<BS, 64, 12, 8, 3>(); return true; }

@@ -44,11 +44,12 @@
 //   Steps that are not whole go unit by unit through the masked build.
 // Rounding: q to 16 bits of its head's range (at most 2^-15 of the largest),
 // p s to f16 (2^-11), the output to bf16; sums, logits, minima in fp32 or exact.
-// Bound: 8 x 131072 tokens (64 heads over 8, head_dim 128) take 250 us, 1.21 GB
-// at 4.8 TB/s, 0.74 of the measured copy rate, and 280 us once the GPU has
-// reached its 1000 W limit (1.86 GHz), after some 100 ms of such calls. Copies
-// alone take 203 us and the math alone 214 us. Integer pipe 53% busy, issue
-// slots 61%.
+// Bound: 8 x 131072 tokens (64 heads over 8, head_dim 128) take 249 us in a burst,
+// 1.21 GB at 4.85 TB/s, 0.74 of the measured copy rate, and 278 us once the GPU has
+// reached its 1000 W limit (1.86 GHz), after some 100 ms of such calls. 332 warp
+// instructions a unit, producers included; integer pipe 53% busy, issue slots 61%.
+// (With one power of two for all groups, which overflowed or lost bits, 325
+// instructions and 246 us; copies alone then took 203 us and the math alone 214.)
 #pragma once
 
 #include <climits>
@@ -148,8 +149,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // j + 4. A mask-or puts a code into the mantissa of 1024, from where it stands
 // (1024 + c, or 1024 + 16 c for the second nibble of a byte), and one packed
 // add or multiply-add makes c - 8 of it, exactly: 5 integer and 4 packed
-// instructions for 8 codes, on different pipes. The mask-or's constants come
-// from registers (an instruction takes one immediate at most).
+// instructions for 8 codes, on different pipes (the conversion of Y. J. Kim et al.,
+// "Who Says Elephants Can't Run: Bringing Large Scale MoE Models into Cloud Scale
+// Production", 2022). The mask-or's constants come from registers (an instruction
+// takes one immediate at most).
 struct CodeBits {
   uint32_t lo4, hi4, k1024;
   __device__ __forceinline__ CodeBits() {

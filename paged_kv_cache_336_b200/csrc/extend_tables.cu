@@ -20,8 +20,9 @@
 // search in the sums. No CTA reads what another writes: a token in a new
 // block takes its id from the queue, not from the table, and the queue's
 // read and written places are disjoint because count + returned <= cap.
-// Bound: launch latency and three dependent global round trips for a decode
-// step (256 sequences 5.2 us); for a prefill wave the sums and table reads that
+// Bound (graph replays; a call's host time is 10 us): launch latency and three
+// dependent global round trips for a decode step (256 sequences 5.2 us); for a
+// prefill wave the sums and table reads that
 // every CTA repeats, then 12 bytes a token (512 sequences, 465,000 tokens, some
 // sequences leaving: 10.3 us).
 #include <cuda_runtime.h>

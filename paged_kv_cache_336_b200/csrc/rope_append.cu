@@ -26,8 +26,9 @@
 // puts its cos and sin in shared memory (one pair a thread, so that all heads
 // of a token share them) and walks the tile's items, each thread loading
 // kUnroll items before it uses any. Bound: HBM (each element read and written
-// once): 16384 tokens of 32 + 8 + 8 heads of 128 in bf16 take 68.4 us, 0.90 of
-// the measured copy rate; for a decode step, launch latency (one token 2.6 us).
+// once): 16384 tokens of 32 + 8 + 8 heads of 128 in bf16 take 68.4 us in graph
+// replays, 0.90 of the measured copy rate (73.6 as calls whose inputs change, 0.84);
+// for a decode step, launch latency (one token 2.8 us, a call 14).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -449,8 +450,10 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// Values of 4-bit rows: a thread takes the same eight dims of K and of V,
-// kGatherUnroll tokens at a time (16384 rows of 8 heads of 128 with their
+// Values of 4-bit rows, one fp32 multiply-add each, which for bf16 is rounded a
+// second time (a product and a minimum far apart would have to be split to save
+// that, at most 2^-24 of the value): a thread takes the same eight dims of K and of
+// V, kGatherUnroll tokens at a time (16384 rows of 8 heads of 128 with their
 // append: 43.4 us for one, 41.0 for two, 41.3 for four). Bound: the 16-bit
 // stores, behind a slot and then a row load.
 constexpr int kGatherUnroll = 2;
