@@ -454,11 +454,11 @@ pa_status_t pa_kv_append_q4(const void* k_new, const void* v_new, int64_t k_stri
 /* ---------------------------------------------------------------------------
  * pa_kv_gather_q4 - reads rows of a 4-bit cache back: k_out, v_out
  * [num_tokens][num_kv_heads][head_dim] in dtype (PA_F32 or PA_BF16), row t the
- * values of slot_mapping[t] (rounded to fp32, for bf16 then to bf16). A row with a negative
- * slot is left as it was. A slot may appear any number of times. The outputs
- * share no memory with one another, the pools or the slots. With slots
- * in token order it lays a sequence out for pa_prefill's 16-bit pools
- * (pa_kv_append) or for inspection.
+ * values of slot_mapping[t] (rounded to fp32, for bf16 then to bf16). A row
+ * with a negative slot is left as it was. A slot may appear any number of
+ * times. The outputs share no memory with one another, the pools or the slots.
+ * With slots in token order it lays a sequence out for pa_prefill's 16-bit
+ * pools (pa_kv_append) or for inspection.
  * ------------------------------------------------------------------------- */
 pa_status_t pa_kv_gather_q4(const void* k_pool, const void* v_pool, const int64_t* slot_mapping,
                             int num_tokens, int num_kv_heads, int head_dim, int block_size,
@@ -536,9 +536,9 @@ pa_status_t pa_rope_frequencies(int rotary_dim, double base, pa_rope_scaling_t s
  * tokens q_stride, k_stride, v_stride elements apart (multiples of 16 bytes:
  * views of one fused product will do). q_out: contiguous
  * [num_tokens][num_q_heads][head_dim]; it may be q itself if that is
- * contiguous, and overlaps nothing else that the call reads or writes. Pools, slots: as for pa_kv_append
- * (pools in dtype). A token with a negative slot is padding: its q is rotated,
- * nothing is cached. num_q_heads may be 0 (q and q_out are then not read).
+ * contiguous, and overlaps nothing else that the call reads or writes. Pools,
+ * slots: as for pa_kv_append (pools in dtype). A token with a negative slot is
+ * padding: its q is rotated, nothing is cached. num_q_heads may be 0 (q and q_out are then not read).
  * rotary_dim: a multiple of 16, 0 .. head_dim; head_dim 64, 128 or 256,
  * block_size 16 or 32.
  *

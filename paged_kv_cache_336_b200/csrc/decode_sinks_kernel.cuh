@@ -5,10 +5,11 @@
 // What is computed: softmax(scale * K_s q) V_s over tokens t < ctx with
 // t >= ctx - window or t < num_sinks; a logit of -inf weighs nothing, and a row of
 // nothing but such logits is zeros, as one without a token.
-// How: paged_decode_stream_kernel's cut (every warp of a persistent grid an equal run of a KV head's list of 16-token
-// units, pieces merged by lse_merge_kernel), over lists that hold the sinks'
-// units and then the window's, so that no other block is read; short windows
-// and small batches are cut sequence by sequence (SinksArgs::seq_cut).
+// How: paged_decode_stream_kernel's cut (every warp of a persistent grid an equal
+// run of a KV head's list of 16-token units, pieces merged by lse_merge_kernel),
+// over lists that hold the sinks' units and then the window's, so that no other
+// block is read; short windows and small batches are cut sequence by sequence
+// (SinksArgs::seq_cut).
 // Bound: 8 sequences of 100,000 to 131,072 tokens, window 4096 + 4, 64 heads
 // over 8 in bf16: 30.4 us in graph replays (floor 20.6): 14 units a warp behind the
 // launch, the lists and the first loads, then the merge.

@@ -22,9 +22,8 @@
 // read and written places are disjoint because count + returned <= cap.
 // Bound (graph replays; a call's host time is 10 us): launch latency and three
 // dependent global round trips for a decode step (256 sequences 5.2 us); for a
-// prefill wave the sums and table reads that
-// every CTA repeats, then 12 bytes a token (512 sequences, 465,000 tokens, some
-// sequences leaving: 10.3 us).
+// prefill wave the sums and table reads that every CTA repeats, then 12 bytes a
+// token (512 sequences, 465,000 tokens, some sequences leaving: 10.3 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
